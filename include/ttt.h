@@ -351,6 +351,94 @@ int ttt_mlp_nc_bwd(const void* q, const void* k, const void* v,
                    const float* eta_tok, float* deta_tok, int loss,
                    int io_dtype, ttt_stream_t stream);
 
+/*
+ * Gated linear recurrence: the delta rule's neighbour that forgets by a gate instead of by
+ * the error.  Per (batch, head), with W float32 [d][d] as above,
+ *   W_t = exp(log_gate[t]) W_{t-1} + eta_t v_t k_t^T,   z_t = W_t q_t,
+ * eta_t = eta or eta * eta_tok[t]: linear attention's state (blog page, section on linear
+ * attention) with a decay per token and head; with a constant decay the retention recurrence
+ * S_t = alpha S_{t-1} + k_t v_t^T (same page), without a gate the dot-product loss at chunk 1.
+ *   log_gate   float32 [B][H][T] or NULL (no decay).  Usually <= 0; -inf (or any value whose
+ *              exponential is 0 in float32) makes the token start anew: what the state held
+ *              before, finite or not, is dropped.  So packed sequences are separated by a
+ *              gate of -inf at each one's first token.
+ *   lengths    int32 [B] device pointer or NULL: batch row b has min(max(lengths[b], 0), T)
+ *              tokens.  Tokens past them are not read; their outputs and gradients are 0.
+ *   q, k, v of tokens within the lengths are finite; a token that is not may make any output
+ *   of its sequence non-finite (up to a gate of -inf in a later block of 64 tokens).
+ * d in {16, 32, 64}, both dtypes, any T >= 0 (T = 0: w_out receives the initial state).  Token
+ * tensors, states, their gradients and the workspace are 16-byte aligned, w0_batch_stride is
+ * a multiple of 4 (TTT_E_INVALID otherwise); eta_tok, log_gate and lengths 4-byte aligned.
+ * The states and every sum are float32; bf16 inputs are multiplied exactly.
+ *
+ * gated_linear_bwd is the backward pass for the upstream gradients dz of z and dw_out of the
+ * final state (float32 [B][H][d][d] or NULL, zero): dq, dk, dv [B][H][T][d] io_dtype,
+ *   dw0       float32 [B][H][d][d], per sequence (sum over b for a state shared over the batch)
+ *   dlog_gate float32 [B][H][T] or NULL (needs log_gate); 0 where the decay is 0
+ *   deta_tok  float32 [B][H][T] or NULL (needs eta_tok).
+ * It needs no output of the forward pass.
+ *
+ * workspace: device memory of at least gated_linear_*_workspace_size(...) bytes (which may be
+ * 0: then it may be NULL), owned by the caller, contents undefined before and after.  One
+ * workspace serves one call at a time.  The calls allocate nothing, so they can be captured
+ * into a graph.
+ */
+size_t gated_linear_fwd_workspace_size(int B, int H, int T, int d, int io_dtype);
+int gated_linear_fwd(const void* q, const void* k, const void* v, const float* log_gate,
+                     const float* w0, long long w0_batch_stride, const int* lengths,
+                     void* z, float* w_out, int B, int H, int T, int d, float eta,
+                     const float* eta_tok, int io_dtype,
+                     void* workspace, size_t workspace_bytes, ttt_stream_t stream);
+size_t gated_linear_bwd_workspace_size(int B, int H, int T, int d, int gated, int io_dtype);
+int gated_linear_bwd(const void* q, const void* k, const void* v, const float* log_gate,
+                     const float* w0, long long w0_batch_stride, const int* lengths,
+                     const void* dz, const float* dw_out,
+                     void* dq, void* dk, void* dv, float* dw0, float* dlog_gate,
+                     int B, int H, int T, int d, float eta,
+                     const float* eta_tok, float* deta_tok, int io_dtype,
+                     void* workspace, size_t workspace_bytes, ttt_stream_t stream);
+
+/*
+ * One token of the recurrence for every sequence, for serving: q, k, v, z [B][H][d], log_gate
+ * and eta_tok [B][H] (or NULL), and the states w float32 [B][H][d][d] updated in place.
+ * Alignment as above; no workspace.
+ */
+int gated_linear_step(const void* q, const void* k, const void* v, const float* log_gate,
+                      float* w, void* z, int B, int H, int d, float eta, const float* eta_tok,
+                      int io_dtype, ttt_stream_t stream);
+
+/*
+ * Norm of the d features of every token, for the places before and after a layer (unit keys
+ * before the delta rule, the norm, gate and residual of the paper's block after it: wmrh.cn
+ * summary of Sun et al. 2024, section 2.2.4):
+ *   y = res + scale act(gate) (norm(x) weight + bias),
+ *   TTT_NORM_LAYER (x - mean) / sqrt(var + eps), biased variance;
+ *   TTT_NORM_RMS   x / sqrt(mean(x^2) + eps);   TTT_NORM_L2  x / sqrt(sum(x^2) + eps).
+ *   x, gate, res, y      [B][H][T][d] io_dtype; gate and res may be NULL (no factor, 0)
+ *   weight, bias, scale  float32 [H][d], each may be NULL (1, 0, 1)
+ *   act  TTT_ACT_NONE (the gate itself), _SILU, _GELU (exact), _SIGMOID; ignored without gate
+ * A model-wide norm is H = 1 with d the model width.  1 <= d <= 16384 (more is
+ * TTT_E_UNSUPPORTED, as are B*H*T > 2^30 and H > 65535), eps > 0 and finite, any alignment of
+ * the elements; 16-byte aligned tensors with rows of whole 16 bytes run faster.  Statistics and
+ * arithmetic are float32, with one rounding at the end.
+ *
+ * token_norm_bwd: for the upstream gradient dy, the gradients of x, weight, bias, gate and
+ * scale (dx always; the others NULL if not wanted, each needs its input; that of res is dy
+ * itself).  dweight, dbias and dscale [H][d] are sums over the batch and the tokens, taken in a
+ * fixed order.  workspace as above, needed for those three.
+ */
+enum { TTT_NORM_LAYER = 0, TTT_NORM_RMS = 1, TTT_NORM_L2 = 2 };
+enum { TTT_ACT_NONE = 0, TTT_ACT_SILU = 1, TTT_ACT_GELU = 2, TTT_ACT_SIGMOID = 3 };
+int token_norm_fwd(const void* x, const float* weight, const float* bias, const void* gate,
+                   const float* scale, const void* res, void* y, int B, int H, int T, int d,
+                   int kind, int act, float eps, int io_dtype, ttt_stream_t stream);
+size_t token_norm_bwd_workspace_size(int B, int H, int T, int d);
+int token_norm_bwd(const void* x, const float* weight, const float* bias, const void* gate,
+                   const float* scale, const void* dy, void* dx, float* dweight, float* dbias,
+                   void* dgate, float* dscale, int B, int H, int T, int d,
+                   int kind, int act, float eps, int io_dtype,
+                   void* workspace, size_t workspace_bytes, ttt_stream_t stream);
+
 /* Message for the calling thread's last non-OK status ("" if none).  Owned by the library;
    valid until the thread's next call into it. */
 const char* ttt_last_error(void);

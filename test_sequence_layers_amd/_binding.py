@@ -55,6 +55,17 @@ SIGNATURES = {
                                _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _i, _i, _vp]),
     "ttt_mlp_nc_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                             _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _i, _i, _vp]),
+    "gated_linear_fwd_workspace_size": (ctypes.c_size_t, [_i, _i, _i, _i, _i]),
+    "gated_linear_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _i,
+                              _vp, ctypes.c_size_t, _vp]),
+    "gated_linear_bwd_workspace_size": (ctypes.c_size_t, [_i, _i, _i, _i, _i, _i]),
+    "gated_linear_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _i, _i, _i, _i, _f, _vp, _vp, _i, _vp, ctypes.c_size_t, _vp]),
+    "gated_linear_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _vp, _i, _vp]),
+    "token_norm_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp]),
+    "token_norm_bwd_workspace_size": (ctypes.c_size_t, [_i, _i, _i, _i]),
+    "token_norm_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                            _i, _i, _i, _i, _i, _i, _f, _i, _vp, ctypes.c_size_t, _vp]),
     "ttt_last_error": (ctypes.c_char_p, []),
     "ttt_abi_version": (_i, []),
     "ttt_set_check_finite": (_i, [_i]),
@@ -613,3 +624,208 @@ def ttt_mlp_ln_fwd(q, k, v, w1, w2, ln_weight, ln_bias, eta, chunk, causal=True,
     float32 [H, d]; every other argument as ttt_mlp_fwd."""
     return _mlp(q, k, v, w1, w2, eta, chunk, causal, (ln_weight, ln_bias, ln_eps), eta_tok, loss,
                 epochs, z, w1_out, w2_out, return_state, stream)
+
+
+# ------------------------------------------------------- gated linear recurrence, token norm
+
+def _on_stream(device, stream):
+    """Context in which torch allocates for the call's stream: outputs and workspaces taken
+    in it are reused in that stream's order."""
+    torch = _torch()
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
+def _optional(t, shape, dtype, device, name):
+    """Pointer of an optional contiguous tensor (None -> NULL)."""
+    if t is None:
+        return None
+    torch = _torch()
+    if (not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype
+            or t.device != device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _pointer(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _workspace(workspace, nbytes, device):
+    """(tensor or None, bytes) of a caller workspace, or of one allocated for this call."""
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    elif (not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous()
+          or workspace.device != device):
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.numel() * workspace.element_size() if workspace is not None else 0
+
+
+def gated_linear_fwd(q, k, v, w0, eta, log_gate=None, *, eta_tok=None, lengths=None, z=None,
+                     w_out=None, return_state=False, workspace=None, stream=None):
+    """Gated linear recurrence W_t = exp(log_gate[t]) W_{t-1} + eta_t v_t k_t^T, z_t = W_t q_t.
+    q, k, v [B,H,T,d] (float32 or bfloat16, d in 16, 32, 64); w0 float32 [H,d,d] (shared over the
+    batch) or [B,H,d,d]; log_gate float32 [B,H,T] (None: no decay; -inf starts a new sequence);
+    eta_tok optional float32 [B,H,T] rate factors; lengths optional int32 [B], tokens of each
+    batch row (z is 0 past them).  workspace: a tensor of at least
+    gated_linear_fwd_workspace_size(...) bytes (None: torch allocates one).  Returns z (and the
+    final state [B,H,d,d] when return_state or w_out is given)."""
+    torch = _torch()
+    lib = load_library()
+    B, H, T, d = _tokens(q, k, v)
+    dev, io = q.device, _io_dtype(q)
+    w0, stride = _state(w0, B, H, (d, d), "w0", dev)
+    gate = _optional(log_gate, (B, H, T), torch.float32, dev, "log_gate")
+    rate = _rates(eta_tok, B, H, T, dev)
+    lens = _optional(lengths, (B,), torch.int32, dev, "lengths")
+    with torch.cuda.device(dev), _on_stream(dev, stream):
+        z = _out(z, (B, H, T, d), q.dtype, dev, "z")
+        if return_state or w_out is not None:
+            w_out = _out(w_out, (B, H, d, d), torch.float32, dev, "w_out")
+        ws, nbytes = _workspace(workspace, lib.gated_linear_fwd_workspace_size(B, H, T, d, io), dev)
+        rc = lib.gated_linear_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate, w0.data_ptr(), stride,
+                                  lens, z.data_ptr(), _pointer(w_out), B, H, T, d, float(eta), rate, io,
+                                  _pointer(ws), nbytes, _stream(dev, None))
+    _check(rc)
+    return (z, w_out) if w_out is not None else z
+
+
+def gated_linear_bwd(q, k, v, w0, eta, log_gate, dz, dw_out=None, *, eta_tok=None, lengths=None,
+                     workspace=None, stream=None):
+    """Gradients of gated_linear_fwd for the upstream gradients dz [B,H,T,d] (dtype of q) and
+    dw_out [B,H,d,d] float32 (or None).  Returns (dq, dk, dv, dw0) with dw0 [B,H,d,d] per
+    sequence (sum it over the batch when w0 is shared), then dlog_gate [B,H,T] if log_gate is
+    given and deta_tok [B,H,T] if eta_tok is.  It needs no output of the forward pass."""
+    torch = _torch()
+    lib = load_library()
+    B, H, T, d = _tokens(q, k, v)
+    dev, io = q.device, _io_dtype(q)
+    w0, stride = _state(w0, B, H, (d, d), "w0", dev)
+    _dz(dz, q, B, H, T, d)
+    dw = _optional(dw_out, (B, H, d, d), torch.float32, dev, "dw_out")
+    gate = _optional(log_gate, (B, H, T), torch.float32, dev, "log_gate")
+    rate = _rates(eta_tok, B, H, T, dev)
+    lens = _optional(lengths, (B,), torch.int32, dev, "lengths")
+    with torch.cuda.device(dev), _on_stream(dev, stream):
+        out = [torch.empty_like(q), torch.empty_like(q), torch.empty_like(q),
+               torch.empty((B, H, d, d), dtype=torch.float32, device=dev)]
+        per_token = lambda x: torch.empty((B, H, T), dtype=torch.float32, device=dev) if x is not None else None
+        dgate, deta = per_token(log_gate), per_token(eta_tok)
+        ws, nbytes = _workspace(workspace, lib.gated_linear_bwd_workspace_size(
+            B, H, T, d, int(dgate is not None), io), dev)
+        rc = lib.gated_linear_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate, w0.data_ptr(), stride,
+                                  lens, dz.data_ptr(), dw, *(x.data_ptr() for x in out), _pointer(dgate),
+                                  B, H, T, d, float(eta), rate, _pointer(deta), io, _pointer(ws), nbytes,
+                                  _stream(dev, None))
+    _check(rc)
+    return tuple(out + [x for x in (dgate, deta) if x is not None])
+
+
+def gated_linear_step(q, k, v, w, eta, log_gate=None, *, eta_tok=None, z=None, stream=None):
+    """One token of gated_linear_fwd for every sequence: q, k, v [B,H,d], log_gate and eta_tok
+    [B,H] float32 (or None), and the states w [B,H,d,d] float32, updated in place.  Returns
+    z [B,H,d]."""
+    torch = _torch()
+    lib = load_library()
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [B, H, d] tensor on a GPU")
+        if t.shape != q.shape or t.dtype != q.dtype or t.device != q.device:
+            raise ValueError("q, k and v must have the same shape, dtype and device")
+    B, H, d = q.shape
+    dev, io = q.device, _io_dtype(q)
+    state = _optional(w, (B, H, d, d), torch.float32, dev, "w")
+    gate = _optional(log_gate, (B, H), torch.float32, dev, "log_gate")
+    rate = _optional(eta_tok, (B, H), torch.float32, dev, "eta_tok")
+    with torch.cuda.device(dev), _on_stream(dev, stream):
+        z = _out(z, (B, H, d), q.dtype, dev, "z")
+        rc = lib.gated_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate, state, z.data_ptr(),
+                                   B, H, d, float(eta), rate, io, _stream(dev, None))
+    _check(rc)
+    return z
+
+
+def gated_linear_fwd_workspace_size(B, H, T, d, dtype) -> int:
+    """Workspace bytes of gated_linear_fwd for token tensors [B,H,T,d] of a torch dtype."""
+    io = TTT_BF16 if dtype == _torch().bfloat16 else TTT_F32
+    return int(load_library().gated_linear_fwd_workspace_size(B, H, T, d, io))
+
+
+def gated_linear_bwd_workspace_size(B, H, T, d, gated, dtype) -> int:
+    """Workspace bytes of gated_linear_bwd; gated: whether log_gate's gradient is taken."""
+    io = TTT_BF16 if dtype == _torch().bfloat16 else TTT_F32
+    return int(load_library().gated_linear_bwd_workspace_size(B, H, T, d, int(bool(gated)), io))
+
+
+_NORMS = {"layer": 0, "rms": 1, "l2": 2}
+_ACTS = {"none": 0, "silu": 1, "gelu": 2, "sigmoid": 3}
+
+
+def _norm_args(x, kind, act):
+    torch = _torch()
+    if not isinstance(x, torch.Tensor) or x.dim() != 4 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous [B, H, T, d] tensor on a GPU")
+    if kind not in _NORMS:
+        raise ValueError(f"kind must be one of {sorted(_NORMS)}, got {kind!r}")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return tuple(x.shape), x.device, _io_dtype(x)
+
+
+def token_norm_fwd(x, kind, eps=1e-6, *, weight=None, bias=None, gate=None, act="silu", scale=None,
+                   res=None, y=None, stream=None):
+    """y = res + scale * act(gate) * (norm(x) * weight + bias) over the d features of every token.
+    x, gate, res [B,H,T,d] (float32 or bfloat16); weight, bias, scale float32 [H,d]; each but x
+    may be None.  kind: "layer", "rms" or "l2" (x / sqrt(sum x^2 + eps)); act: "silu", "gelu"
+    (exact), "sigmoid" or "none" (the gate itself)."""
+    torch = _torch()
+    lib = load_library()
+    (B, H, T, d), dev, io = _norm_args(x, kind, act)
+    par = [_optional(t, (H, d), torch.float32, dev, n)
+           for t, n in ((weight, "weight"), (bias, "bias"), (scale, "scale"))]
+    gp, rp = (_optional(t, x.shape, x.dtype, dev, n) for t, n in ((gate, "gate"), (res, "res")))
+    with torch.cuda.device(dev), _on_stream(dev, stream):
+        y = _out(y, x.shape, x.dtype, dev, "y")
+        rc = lib.token_norm_fwd(x.data_ptr(), par[0], par[1], gp, par[2], rp, y.data_ptr(), B, H, T, d,
+                                _NORMS[kind], _ACTS[act], float(eps), io, _stream(dev, None))
+    _check(rc)
+    return y
+
+
+def token_norm_bwd(x, dy, kind, eps=1e-6, *, weight=None, bias=None, gate=None, act="silu",
+                   scale=None, workspace=None, stream=None):
+    """Gradients of token_norm_fwd for the upstream gradient dy (dtype of x): returns
+    (dx, dweight, dbias, dgate, dscale), None for each input that is None; that of res is dy
+    itself.  dweight, dbias and dscale [H,d] float32 are sums over the batch and the tokens."""
+    torch = _torch()
+    lib = load_library()
+    (B, H, T, d), dev, io = _norm_args(x, kind, act)
+    dyp = _optional(dy, x.shape, x.dtype, dev, "dy")
+    if dyp is None:
+        raise ValueError("dy must be given")
+    named = ((weight, "weight"), (bias, "bias"), (scale, "scale"))
+    par = [_optional(t, (H, d), torch.float32, dev, n) for t, n in named]
+    gp = _optional(gate, x.shape, x.dtype, dev, "gate")
+    with torch.cuda.device(dev), _on_stream(dev, stream):
+        dx = torch.empty_like(x)
+        dpar = [torch.empty((H, d), dtype=torch.float32, device=dev) if t is not None else None
+                for t, _ in named]
+        dg = torch.empty_like(x) if gate is not None else None
+        need = lib.token_norm_bwd_workspace_size(B, H, T, d) if any(t is not None for t in dpar) else 0
+        ws, nbytes = _workspace(workspace, need, dev)
+        rc = lib.token_norm_bwd(x.data_ptr(), par[0], par[1], gp, par[2], dyp, dx.data_ptr(),
+                                _pointer(dpar[0]), _pointer(dpar[1]), _pointer(dg), _pointer(dpar[2]),
+                                B, H, T, d, _NORMS[kind], _ACTS[act], float(eps), io, _pointer(ws),
+                                nbytes, _stream(dev, None))
+    _check(rc)
+    return dx, dpar[0], dpar[1], dg, dpar[2]
+
+
+def token_norm_bwd_workspace_size(B, H, T, d) -> int:
+    """Workspace bytes of token_norm_bwd (when a parameter's gradient is taken)."""
+    return int(load_library().token_norm_bwd_workspace_size(B, H, T, d))

@@ -168,6 +168,53 @@ struct MlpBwdArgs {
   float* dln_b = nullptr;
 };
 
+// Gated linear recurrence W_t = exp(gate_t) W_{t-1} + e_t v_t k_t^T, z_t = W_t q_t (dense d x d
+// states; forward, backward and the single-token form).
+struct GatedArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* gate;     // log decays [B][H][T] or null (no decay)
+  const float* w0;
+  long long w0_batch_stride;  // in floats
+  const int* lengths;    // tokens per batch row [B] or null (T)
+  int B, H, T;
+  float eta;
+  const float* eta_tok;  // per-token rate factors [B][H][T] or null
+  void* z = nullptr;     // forward: outputs and final states (or null)
+  float* w_out = nullptr;
+  const void* dz = nullptr;  // backward: upstream gradients (dw_out or null) and outputs
+  const float* dw_out = nullptr;
+  void* dq = nullptr;
+  void* dk = nullptr;
+  void* dv = nullptr;
+  float* dw0 = nullptr;
+  float* dgate = nullptr;
+  float* deta_tok = nullptr;
+  double* ws_end = nullptr;  // workspace of the gate's gradient
+  float* ws_tok = nullptr;
+};
+
+// y = res + scale act(gate) (norm(x) weight + bias) over the d features of a token; every
+// pointer but x and y (dy and dx) may be null.
+struct NormArgs {
+  const void* x;
+  const float* weight;  // [H][d], as bias and scale
+  const float* bias;
+  const void* gate;     // [B][H][T][d], as res, y and their gradients
+  const float* scale;
+  const void* res;
+  void* y;
+  int B, H, T, d, kind, act;
+  float eps;
+  const void* dy = nullptr;  // backward
+  void* dx = nullptr;
+  float* dweight = nullptr;  // [H][d]
+  float* dbias = nullptr;
+  void* dgate = nullptr;
+  float* dscale = nullptr;
+};
+
 // Host-side launchers (return a hipError_t; argument checks are done by the caller).
 hipError_t launch_linear_generic(const LinearArgs& a, bool bf16_io, hipStream_t s);
 hipError_t launch_mlp_generic(const MlpArgs& a, bool bf16_io, float* workspace, hipStream_t s);
@@ -251,6 +298,20 @@ hipError_t launch_nc_bwd(bool mlp, const void* q, const void* k, const void* v, 
                          void* dq, void* dk, void* dv, float* dw1, float* dw2, float* deta_tok,
                          float* ws, int B, int H, int T, int d, int h, int chunk, int epochs,
                          float eta, int dot_loss, bool bf16_io, hipStream_t s);
+
+// gated linear recurrence (d in {16, 32, 64}; pointers 16-byte aligned)
+size_t gated_fwd_workspace_bytes(int B, int H, int T, int d, bool bf16_io);
+size_t gated_bwd_workspace_bytes(int B, int H, int T, int d, bool gated, bool bf16_io);
+hipError_t launch_gated_fwd(GatedArgs a, int d, bool bf16_io, void* ws, hipStream_t s);
+hipError_t launch_gated_bwd(GatedArgs a, int d, bool bf16_io, void* ws, hipStream_t s);
+// one token per sequence, w [B][H][d][d] updated in place
+hipError_t launch_gated_step(const GatedArgs& a, float* w, int d, bool bf16_io, hipStream_t s);
+
+// token norm (any d up to kTokenNormMaxDim); the parameters' gradients need the workspace
+constexpr int kTokenNormMaxDim = 16384;
+size_t token_norm_bwd_workspace_bytes(int B, int H, int T, int d);
+hipError_t launch_token_norm_fwd(const NormArgs& a, bool bf16_io, hipStream_t s);
+hipError_t launch_token_norm_bwd(const NormArgs& a, bool bf16_io, void* ws, hipStream_t s);
 
 // dst[b][h][:] = src + b * batch_stride + h * per_head (the state when T = 0); zeros when
 // src is null.

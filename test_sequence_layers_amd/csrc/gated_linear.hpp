@@ -1,0 +1,84 @@
+// Shared pieces of the gated linear recurrence's kernels (gated_linear*.hip):
+//
+//   W_t = a_t W_{t-1} + e_t v_t k_t^T,  z_t = W_t q_t,  a_t = exp(g_t),  e_t = eta eta_tok[t],
+//
+// taken kGlChunk tokens at a time.  With b_u = sum of g from the chunk's start through token u,
+// W the state before the chunk and C its last token:
+//   z_u   = sum_{s <= u} exp(b_u - b_s) e_s (q_u . k_s) v_s + exp(b_u) W q_u,
+//   W_end = exp(b_C) W + sum_s exp(b_C - b_s) e_s v_s k_s^T.
+#pragma once
+
+#include "common.hpp"
+
+namespace ttt {
+
+constexpr int kGlChunk = 64;             // tokens per chunk
+constexpr int kGlPitch = kGlChunk + 4;   // row pitch (floats) of matrices with a column per token
+
+// The decays of one chunk in LDS, one entry per token.
+struct GlDecays {
+  float bh[kGlChunk], bl[kGlChunk];  // b_u / ln 2 as the sum of two floats
+  float e[kGlChunk];                 // e_s (0 past the sequence)
+  float from[kGlChunk];              // exp(b_u): from the chunk's start
+  float to[kGlChunk];                // exp(b_C - b_s): to the chunk's end
+  float whole[4];                    // exp(b_C) (first entry)
+};
+
+// Base-2 logarithms below kGlNever count as kGlNever: 2^-4096 is 0 in float32 as the decay
+// itself is, and sums over a chunk stay below 2^18, so that two floats hold them to 2^-29 and
+// tokens after a forgotten one (g = -inf, or the type's lowest value) keep exact differences.
+constexpr double kGlNever = -4096.0;
+
+// One wave, lane = token: g is the token's log decay (0 past the sequence).  The prefix sum
+// runs in 64 bits: b_u - b_s is a small difference of sums that may be large.
+__device__ __forceinline__ void gl_decays(float g, float e, GlDecays* d, int lane) {
+  double x = static_cast<double>(g) * 1.4426950408889634;
+  if (x < kGlNever) x = kGlNever;  // a NaN stays one
+#pragma unroll
+  for (int o = 1; o < kGlChunk; o <<= 1) {
+    const double y = __shfl_up(x, o, 64);
+    if (lane >= o) x += y;
+  }
+  const double last = __shfl(x, kGlChunk - 1, 64);
+  const float h = static_cast<float>(x);
+  d->bh[lane] = h;
+  d->bl[lane] = static_cast<float>(x - h);
+  d->e[lane] = e;
+  d->from[lane] = __builtin_amdgcn_exp2f(h);
+  d->to[lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - x));
+  if (lane == 0) d->whole[0] = __builtin_amdgcn_exp2f(static_cast<float>(last));
+}
+
+// exp(b_u - b_s)
+__device__ __forceinline__ float gl_between(float uh, float ul, float sh, float sl) {
+  return __builtin_amdgcn_exp2f((uh - sh) + (ul - sl));
+}
+
+// f x, with what a decay of 0 drops left out whatever it is (a state that is not finite too)
+__device__ __forceinline__ float gl_keep(float f, float x) { return f == 0.0f ? 0.0f : f * x; }
+
+typedef float gl_f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t gl_u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t gl_u4 __attribute__((ext_vector_type(4)));
+
+// Loads and stores through buffer resources whose range ends at the last valid token: rows
+// past it read as zero and their stores are dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t gl_span(const void* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes > 0 ? bytes : 0, 0x00020000);
+}
+
+// Workgroup barrier for LDS traffic: this wave's LDS accesses are complete, then all waves
+// meet.  Global loads and stores stay in flight (waves exchange data through LDS only).
+__device__ __forceinline__ void gl_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0), vmcnt/expcnt unconstrained
+  __asm__ __volatile__("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  __asm__ __volatile__("" ::: "memory");
+}
+
+// tokens of a sequence: lengths[b] held to [0, T], or T
+__device__ __forceinline__ int gl_length(const int* lengths, int b, int T) {
+  return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
+}  // namespace ttt

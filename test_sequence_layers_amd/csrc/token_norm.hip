@@ -1,0 +1,455 @@
+// Norm of the d features of every token with gate, scale and residual, forward and backward:
+//
+//   y = res + scale act(gate) n,  n = xh weight + bias,  xh = (x - m) r,
+//   layer: m = mean(x), r = 1 / sqrt(mean((x - m)^2) + eps);
+//   rms:   m = 0, r = 1 / sqrt(mean(x^2) + eps);   l2: m = 0, r = 1 / sqrt(sum(x^2) + eps).
+//
+// Backward, with A = act(gate) (1 without a gate), s = scale (1 without):
+//   dgate = dy s n act'(gate),  dscale = sum dy A n,  t = dy s A,  dbias = sum t,
+//   dweight = sum t xh,  u = t weight,  dx = r (u - mean(u) - xh mean(u xh))
+// (rms: without mean(u); l2: the sum of u xh in place of its mean), sums over the batch and
+// the tokens.
+//
+// Both are bound by HBM: each tensor passes once.  A row lives in the registers of LPR lanes
+// (part of a wave, a wave, or a workgroup), NV vectors of W elements a lane, so its statistics
+// need no second read; everything between load and store is float32.
+#include <initializer_list>
+#include <type_traits>
+
+#include "gated_linear.hpp"
+
+namespace ttt {
+namespace {
+
+enum { kLayer = 0, kRms = 1, kL2 = 2 };
+enum { kActNone = 0, kSilu = 1, kGelu = 2, kSigmoid = 3 };
+
+// W consecutive elements (16 bytes, or one)
+template <typename IO, int W>
+__device__ __forceinline__ void load_vec(const IO* p, float* x) {
+  if constexpr (W == 1) {
+    x[0] = to_f32(p[0]);
+  } else {
+    if constexpr (W == 4) {
+      const gl_f4 y = *reinterpret_cast<const gl_f4*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = y[i];
+    } else {
+      const gl_u4 y = *reinterpret_cast<const gl_u4*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __builtin_bit_cast(float, y[i] << 16);
+        x[2 * i + 1] = __builtin_bit_cast(float, y[i] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+template <typename IO, int W>
+__device__ __forceinline__ void store_vec(IO* p, const float* x) {
+  if constexpr (W == 1) {
+    p[0] = from_f32<IO>(x[0]);
+  } else {
+    typedef IO vec __attribute__((ext_vector_type(W)));
+    vec y;
+#pragma unroll
+    for (int i = 0; i < W; ++i) y[i] = from_f32<IO>(x[i]);
+    *reinterpret_cast<vec*>(p) = y;
+  }
+}
+// float32 parameters of the same W columns (16-byte loads when W > 1)
+template <int W>
+__device__ __forceinline__ void load_par(const float* p, float* x) {
+  if constexpr (W == 1) {
+    x[0] = p[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const gl_f4 y = *reinterpret_cast<const gl_f4*>(p + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i + j] = y[j];
+    }
+  }
+}
+
+__device__ __forceinline__ float act_(int act, float g) {
+  return act == kSilu ? silu_(g) : act == kGelu ? gelu_(g) : act == kSigmoid ? sigmoidf_(g) : g;
+}
+__device__ __forceinline__ void act_grad(int act, float g, float* a, float* da) {
+  if (act == kSilu || act == kSigmoid) {
+    const float s = sigmoidf_(g);
+    *a = act == kSilu ? g * s : s;
+    *da = act == kSilu ? s * (1.0f + g * (1.0f - s)) : s * (1.0f - s);
+  } else {
+    *a = act == kGelu ? gelu_(g) : g;
+    *da = act == kGelu ? dgelu_(g) : 1.0f;
+  }
+}
+
+// Sum over the lanes of a row; for rows of a whole workgroup through LDS (`red`, one slot per
+// wave, used alternately so that one barrier a sum is enough).
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x, float (*red)[16], int* turn) {
+  x = group_sum<(LPR < 64 ? LPR : 64)>(x);
+  if constexpr (LPR > 64) {
+    float* slot = red[*turn & 1];
+    ++*turn;
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = 0.0f;
+#pragma unroll
+    for (int i = 0; i < LPR / 64; ++i) x += slot[i];
+  }
+  return x;
+}
+
+// The row in registers: x becomes xh; returns r.
+template <int LPR, int N>
+__device__ __forceinline__ float normalise(float* x, const bool* have, int W, int kind, int d, float eps,
+                                           float (*red)[16], int* turn) {
+  const float inv = kind == kL2 ? 1.0f : 1.0f / d;
+  if (kind == kLayer) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += x[i];
+    const float m = row_sum<LPR>(sum, red, turn) * inv;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = have[i / W] ? x[i] - m : 0.0f;
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) ss += x[i] * x[i];
+  const float r = 1.0f / sqrtf(row_sum<LPR>(ss, red, turn) * inv + eps);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] *= r;
+  return r;
+}
+
+template <int LPR> struct Block {
+  static constexpr int kThreads = LPR > 256 ? LPR : 256;
+  static constexpr int kRows = kThreads / LPR;  // rows a workgroup holds at once
+};
+
+// A workgroup takes `passes` x kRows consecutive rows.
+template <typename IO, int W, int LPR, int NV>
+__global__ __launch_bounds__(Block<LPR>::kThreads) void norm_fwd_kernel(NormArgs a, int rows, int passes) {
+  __shared__ float red[2][16];
+  int turn = 0;
+  constexpr int RB = Block<LPR>::kRows;
+  const int in_row = threadIdx.x % LPR, group = threadIdx.x / LPR;
+  const IO* xp = static_cast<const IO*>(a.x);
+  const IO* gp = static_cast<const IO*>(a.gate);
+  const IO* rp = static_cast<const IO*>(a.res);
+  IO* yp = static_cast<IO*>(a.y);
+  for (int p = 0; p < passes; ++p) {
+    const long long first = (static_cast<long long>(blockIdx.x) * passes + p) * RB;
+    if (first >= rows) return;  // the same for every thread
+    const int row = static_cast<int>(first) + group;
+    const bool live = row < rows;
+    const size_t base = static_cast<size_t>(live ? row : 0) * a.d;
+    const size_t hb = static_cast<size_t>((live ? row : 0) / a.T % a.H) * a.d;
+    float x[NV * W], gt[NV * W], rs[NV * W];
+    bool have[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int col = (v * LPR + in_row) * W;
+      have[v] = live && col < a.d;
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[v * W + i] = gt[v * W + i] = rs[v * W + i] = 0.0f;
+      if (have[v]) {
+        load_vec<IO, W>(xp + base + col, x + v * W);
+        if (gp) load_vec<IO, W>(gp + base + col, gt + v * W);
+        if (rp) load_vec<IO, W>(rp + base + col, rs + v * W);
+      }
+    }
+    normalise<LPR, NV * W>(x, have, W, a.kind, a.d, a.eps, red, &turn);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (!have[v]) continue;
+      const int col = (v * LPR + in_row) * W;
+      float par[W], y[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) y[i] = x[v * W + i];
+      if (a.weight) {
+        load_par<W>(a.weight + hb + col, par);
+#pragma unroll
+        for (int i = 0; i < W; ++i) y[i] *= par[i];
+      }
+      if (a.bias) {
+        load_par<W>(a.bias + hb + col, par);
+#pragma unroll
+        for (int i = 0; i < W; ++i) y[i] += par[i];
+      }
+      if (gp) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) y[i] *= act_(a.act, gt[v * W + i]);
+      }
+      if (a.scale) {
+        load_par<W>(a.scale + hb + col, par);
+#pragma unroll
+        for (int i = 0; i < W; ++i) y[i] *= par[i];
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) y[i] += rs[v * W + i];
+      store_vec<IO, W>(yp + base + col, y);
+    }
+  }
+}
+
+// Workgroup (part, head) takes an even share of the head's B T rows, and leaves its sums of the
+// parameters' gradients in part[head][part][3][d].
+template <typename IO, int W, int LPR, int NV>
+__global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs a, float* part) {
+  extern __shared__ float sums[];  // [3][d] (rows of a wave or less)
+  __shared__ float red[2][16];
+  int turn = 0;
+  constexpr int RB = Block<LPR>::kRows, N = NV * W;
+  const int in_row = threadIdx.x % LPR, group = threadIdx.x / LPR;
+  const int head = blockIdx.y;
+  const long long all = static_cast<long long>(a.B) * a.T;
+  const long long from = all * blockIdx.x / gridDim.x, to = all * (blockIdx.x + 1) / gridDim.x;
+  const IO* xp = static_cast<const IO*>(a.x);
+  const IO* gp = static_cast<const IO*>(a.gate);
+  const IO* dyp = static_cast<const IO*>(a.dy);
+  IO* dxp = static_cast<IO*>(a.dx);
+  IO* dgp = static_cast<IO*>(a.dgate);
+  const size_t hb = static_cast<size_t>(head) * a.d;
+  float sw[N], sb[N], ss[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) sw[i] = sb[i] = ss[i] = 0.0f;
+  for (long long first = from; first < to; first += RB) {
+    const long long i0 = first + group;
+    const bool live = i0 < to;
+    const long long bt = live ? i0 : from;
+    const size_t base = (static_cast<size_t>(bt / a.T * a.H + head) * a.T + bt % a.T) * a.d;
+    float x[N], dy[N], gt[N];
+    bool have[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int col = (v * LPR + in_row) * W;
+      have[v] = live && col < a.d;
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[v * W + i] = dy[v * W + i] = gt[v * W + i] = 0.0f;
+      if (have[v]) {
+        load_vec<IO, W>(xp + base + col, x + v * W);
+        load_vec<IO, W>(dyp + base + col, dy + v * W);
+        if (gp) load_vec<IO, W>(gp + base + col, gt + v * W);
+      }
+    }
+    const float r = normalise<LPR, N>(x, have, W, a.kind, a.d, a.eps, red, &turn);
+    float m1 = 0.0f, m2 = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (!have[v]) continue;
+      const int col = (v * LPR + in_row) * W;
+      float wt[W], bs[W], sc[W], dg[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        wt[i] = sc[i] = 1.0f;
+        bs[i] = 0.0f;
+      }
+      if (a.weight) load_par<W>(a.weight + hb + col, wt);
+      if (a.bias) load_par<W>(a.bias + hb + col, bs);
+      if (a.scale) load_par<W>(a.scale + hb + col, sc);
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const int j = v * W + i;
+        const float n = x[j] * wt[i] + bs[i];
+        float act = 1.0f, dact = 0.0f;
+        if (gp) act_grad(a.act, gt[j], &act, &dact);
+        ss[j] += dy[j] * act * n;
+        const float t0 = dy[j] * sc[i], t = t0 * act;
+        dg[i] = t0 * n * dact;
+        sb[j] += t;
+        sw[j] += t * x[j];
+        dy[j] = t * wt[i];
+        m1 += dy[j];
+        m2 += dy[j] * x[j];
+      }
+      if (dgp) store_vec<IO, W>(dgp + base + col, dg);
+    }
+    const float inv = 1.0f / a.d;
+    m2 = row_sum<LPR>(m2, red, &turn) * (a.kind == kL2 ? 1.0f : inv);
+    m1 = a.kind == kLayer ? row_sum<LPR>(m1, red, &turn) * inv : 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (!have[v]) continue;
+      float dx[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) dx[i] = r * (dy[v * W + i] - m1 - x[v * W + i] * m2);
+      store_vec<IO, W>(dxp + base + (v * LPR + in_row) * W, dx);
+    }
+  }
+  if (!part) return;
+  // rows of one workgroup: lanes that hold the same columns, then wave after wave
+  if constexpr (LPR < 64) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int o = LPR; o < 64; o <<= 1) {
+        sw[i] += __shfl_xor(sw[i], o, 64);
+        sb[i] += __shfl_xor(sb[i], o, 64);
+        ss[i] += __shfl_xor(ss[i], o, 64);
+      }
+    }
+  }
+  float* out = part + (static_cast<size_t>(head) * gridDim.x + blockIdx.x) * 3 * a.d;
+  if constexpr (LPR > 64) {  // one row at a time: the registers hold the workgroup's sums
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int col = (v * LPR + in_row) * W;
+      if (col < a.d) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          out[col + i] = sw[v * W + i];
+          out[a.d + col + i] = sb[v * W + i];
+          out[2 * a.d + col + i] = ss[v * W + i];
+        }
+      }
+    }
+  } else {
+    for (int w = 0; w < Block<LPR>::kThreads / 64; ++w) {
+      if (static_cast<int>(threadIdx.x & 63) < LPR && static_cast<int>(threadIdx.x >> 6) == w) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int col = (v * LPR + in_row) * W;
+          if (col < a.d) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+              const int j = v * W + i;
+              sums[col + i] = w ? sums[col + i] + sw[j] : sw[j];
+              sums[a.d + col + i] = w ? sums[a.d + col + i] + sb[j] : sb[j];
+              sums[2 * a.d + col + i] = w ? sums[2 * a.d + col + i] + ss[j] : ss[j];
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < 3 * a.d; i += Block<LPR>::kThreads) out[i] = sums[i];
+  }
+}
+
+// out[head][col] = sum over the parts, in order (64 bits): 64 columns a workgroup, four
+// quarters of the parts each, joined through LDS.
+__global__ __launch_bounds__(256) void norm_sum_kernel(NormArgs a, const float* part, int parts) {
+  __shared__ double quarter[4][64];
+  const int col = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  const int head = blockIdx.y, which = blockIdx.z;
+  float* out = which == 0 ? a.dweight : which == 1 ? a.dbias : a.dscale;
+  if (!out) return;
+  double s = 0.0;
+  if (col < a.d) {
+    const float* p = part + static_cast<size_t>(head) * parts * 3 * a.d + static_cast<size_t>(which) * a.d + col;
+    for (int i = parts * q / 4; i < parts * (q + 1) / 4; ++i) s += p[static_cast<size_t>(i) * 3 * a.d];
+  }
+  quarter[q][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (q == 0 && col < a.d)
+    out[static_cast<size_t>(head) * a.d + col] =
+        static_cast<float>((quarter[0][threadIdx.x] + quarter[1][threadIdx.x]) + (quarter[2][threadIdx.x] + quarter[3][threadIdx.x]));
+}
+
+// 16-byte vectors need whole vectors in a row and aligned tensors and parameters
+bool aligned16(std::initializer_list<const void*> ps) {
+  uintptr_t bits = 0;
+  for (const void* p : ps) bits |= reinterpret_cast<uintptr_t>(p);
+  return (bits & 15) == 0;
+}
+bool vectors(const NormArgs& a, int es) {
+  return a.d % (16 / es) == 0 &&
+         aligned16({a.x, a.weight, a.bias, a.gate, a.scale, a.res, a.y, a.dy, a.dx, a.dgate});
+}
+
+// f(W, LPR, NV) for the smallest layout that holds a row of d elements
+template <int W, typename F>
+hipError_t layout(int d, F f) {
+  const int n = (d + W - 1) / W;
+#define TTT_TRY(lpr, nv) \
+  if (n <= lpr * nv) return f(std::integral_constant<int, W>(), std::integral_constant<int, lpr>(), std::integral_constant<int, nv>())
+  if constexpr (W > 1) {
+    TTT_TRY(2, 1);
+    TTT_TRY(4, 1);
+    TTT_TRY(8, 1);
+    TTT_TRY(16, 1);
+    TTT_TRY(32, 1);
+  }
+  TTT_TRY(64, 1);
+  TTT_TRY(64, 2);
+  TTT_TRY(64, 4);
+  if constexpr (W == 1) TTT_TRY(64, 8);
+  TTT_TRY(256, 2);
+  TTT_TRY(256, 4);
+  if constexpr (W <= 4) TTT_TRY(256, 8);
+  if constexpr (W == 8) TTT_TRY(1024, 2);
+  TTT_TRY(1024, 4);
+  if constexpr (W == 1) {
+    TTT_TRY(1024, 8);
+    TTT_TRY(1024, 16);
+  }
+#undef TTT_TRY
+  return hipErrorInvalidValue;
+}
+
+template <typename IO, int W, int LPR, int NV>
+hipError_t run_fwd(const NormArgs& a, hipStream_t s) {
+  constexpr int RB = Block<LPR>::kRows;
+  const long long rows = static_cast<long long>(a.B) * a.H * a.T;
+  const long long groups = (rows + RB - 1) / RB;
+  // several passes share a workgroup's start once there are workgroups enough
+  const int passes = groups >= 8192 ? 4 : groups >= 4096 ? 2 : 1;
+  norm_fwd_kernel<IO, W, LPR, NV><<<dim3(static_cast<unsigned>((groups + passes - 1) / passes)), dim3(Block<LPR>::kThreads), 0, s>>>(
+      a, static_cast<int>(rows), passes);
+  return hipGetLastError();
+}
+
+// Shares of a head's rows in the backward pass: workgroups enough to fill the chip (about 1024),
+// each with 16 rows at least so that its sums stay small next to its rows.
+int bwd_parts(int B, int H, int T) {
+  const long long rows = static_cast<long long>(B) * T;
+  long long parts = (1024 + H - 1) / H;
+  if (parts > (rows + 15) / 16) parts = (rows + 15) / 16;
+  return static_cast<int>(parts < 1 ? 1 : parts);
+}
+
+template <typename IO, int W, int LPR, int NV>
+hipError_t run_bwd(const NormArgs& a, void* ws, hipStream_t s) {
+  const int parts = bwd_parts(a.B, a.H, a.T);
+  const bool sums = a.dweight || a.dbias || a.dscale;
+  const int lds = sums && LPR <= 64 ? 3 * a.d * static_cast<int>(sizeof(float)) : 0;  // 24 KB at most
+  const auto fn = norm_bwd_kernel<IO, W, LPR, NV>;
+  fn<<<dim3(parts, a.H), dim3(Block<LPR>::kThreads), lds, s>>>(a, sums ? static_cast<float*>(ws) : nullptr);
+  return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t bwd_io(const NormArgs& a, void* ws, hipStream_t s) {
+  auto go = [&](auto w, auto lpr, auto nv) { return run_bwd<IO, w.value, lpr.value, nv.value>(a, ws, s); };
+  constexpr int W = 16 / static_cast<int>(sizeof(IO));
+  hipError_t e = vectors(a, sizeof(IO)) ? layout<W>(a.d, go) : layout<1>(a.d, go);
+  if (e != hipSuccess || !(a.dweight || a.dbias || a.dscale)) return e;
+  norm_sum_kernel<<<dim3((a.d + 63) / 64, a.H, 3), dim3(256), 0, s>>>(a, static_cast<const float*>(ws), bwd_parts(a.B, a.H, a.T));
+  return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t fwd_io(const NormArgs& a, hipStream_t s) {
+  auto go = [&](auto w, auto lpr, auto nv) { return run_fwd<IO, w.value, lpr.value, nv.value>(a, s); };
+  constexpr int W = 16 / static_cast<int>(sizeof(IO));
+  return vectors(a, sizeof(IO)) ? layout<W>(a.d, go) : layout<1>(a.d, go);
+}
+
+}  // namespace
+
+size_t token_norm_bwd_workspace_bytes(int B, int H, int T, int d) {
+  return static_cast<size_t>(bwd_parts(B, H, T)) * H * 3 * d * sizeof(float);
+}
+
+hipError_t launch_token_norm_fwd(const NormArgs& a, bool bf16_io, hipStream_t s) {
+  return bf16_io ? fwd_io<bf16>(a, s) : fwd_io<float>(a, s);
+}
+
+hipError_t launch_token_norm_bwd(const NormArgs& a, bool bf16_io, void* ws, hipStream_t s) {
+  return bf16_io ? bwd_io<bf16>(a, ws, s) : bwd_io<float>(a, ws, s);
+}
+
+}  // namespace ttt

@@ -415,6 +415,69 @@ long long tok(int B, int H, int T, int d) { return static_cast<long long>(B) * H
 long long per_seq(int B, int H, long long n) { return static_cast<long long>(B) * H * n; }
 int io_bytes(int io_dtype) { return io_dtype == TTT_BF16 ? 2 : 4; }
 
+// ---- gated linear recurrence ----
+
+bool all_aligned(std::initializer_list<const void*> ps, uintptr_t bytes) {
+  uintptr_t bits = 0;
+  for (const void* p : ps) bits |= reinterpret_cast<uintptr_t>(p);
+  return (bits & (bytes - 1)) == 0;
+}
+
+// the checks of gated_linear_fwd, _bwd and _step (T = 1); the token pointers may be null when T = 0
+int check_gated(const char* fn, std::initializer_list<const void*> tokens,
+                std::initializer_list<const void*> states, const float* log_gate,
+                const int* lengths, int B, int H, int T, int d, float eta, const float* eta_tok,
+                int io_dtype) {
+  if (B <= 0 || H <= 0 || d <= 0 || T < 0)
+    return fail(TTT_E_INVALID, "%s: sizes must be positive (B=%d H=%d T=%d d=%d)", fn, B, H, T, d);
+  if (io_dtype != TTT_F32 && io_dtype != TTT_BF16)
+    return fail(TTT_E_INVALID, "%s: unknown io_dtype %d", fn, io_dtype);
+  if (!std::isfinite(eta)) return fail(TTT_E_INVALID, "%s: eta must be finite", fn);
+  if (!all_aligned({eta_tok, log_gate, lengths}, 4))
+    return fail(TTT_E_INVALID, "%s: log_gate, eta_tok and lengths must be 4-byte aligned", fn);
+  for (const void* p : tokens)
+    if (T > 0 && !p) return fail(TTT_E_INVALID, "%s: token tensors must be non-null", fn);
+  if (!all_aligned(tokens, 16) || !all_aligned(states, 16))
+    return fail(TTT_E_INVALID, "%s: token tensors and states must be 16-byte aligned", fn);
+  if (d != 16 && d != 32 && d != 64)
+    return fail(TTT_E_UNSUPPORTED, "%s: d=%d not supported (16, 32, 64)", fn, d);
+  if (static_cast<long long>(B) * H > 0x3fffffffLL || !fits_int64(B, H, T > 0 ? T : 1, 4LL * d * d))
+    return fail(TTT_E_INVALID, "%s: B*H*T*d overflows", fn);
+  if (static_cast<long long>(B) * H * (T / 64 + 1LL) > 0x7fffffffLL)
+    return fail(TTT_E_UNSUPPORTED, "%s: B*H*T/64 exceeds the grid limit", fn);
+  return TTT_OK;
+}
+
+int check_workspace(const char* fn, const void* ws, size_t have, size_t need) {
+  if (need == 0) return TTT_OK;
+  if (!ws || have < need)
+    return fail(TTT_E_INVALID, "%s: workspace of %zu bytes, this call needs %zu", fn, ws ? have : size_t(0), need);
+  if ((reinterpret_cast<uintptr_t>(ws) & 15) != 0)
+    return fail(TTT_E_INVALID, "%s: workspace must be 16-byte aligned", fn);
+  return TTT_OK;
+}
+
+// ---- token norm ----
+
+int check_norm(const char* fn, const void* x, const void* y, int B, int H, int T, int d, int kind,
+               int act, float eps, int io_dtype) {
+  if (B <= 0 || H <= 0 || d <= 0 || T < 0)
+    return fail(TTT_E_INVALID, "%s: sizes must be positive (B=%d H=%d T=%d d=%d)", fn, B, H, T, d);
+  if (io_dtype != TTT_F32 && io_dtype != TTT_BF16)
+    return fail(TTT_E_INVALID, "%s: unknown io_dtype %d", fn, io_dtype);
+  if (kind < TTT_NORM_LAYER || kind > TTT_NORM_L2) return fail(TTT_E_INVALID, "%s: unknown norm %d", fn, kind);
+  if (act < TTT_ACT_NONE || act > TTT_ACT_SIGMOID)
+    return fail(TTT_E_INVALID, "%s: unknown activation %d", fn, act);
+  if (!std::isfinite(eps) || !(eps > 0.0f))
+    return fail(TTT_E_INVALID, "%s: eps must be finite and positive", fn);
+  if (T > 0 && (!x || !y)) return fail(TTT_E_INVALID, "%s: token tensors must be non-null", fn);
+  if (d > ttt::kTokenNormMaxDim)
+    return fail(TTT_E_UNSUPPORTED, "%s: d=%d not supported (at most %d)", fn, d, ttt::kTokenNormMaxDim);
+  if (H > 65535 || !fits_int64(B, H, T > 0 ? T : 1, 1) || static_cast<long long>(B) * H * T > (1LL << 30))
+    return fail(TTT_E_UNSUPPORTED, "%s: H > 65535 or B*H*T > 2^30", fn);
+  return TTT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1051,6 +1114,143 @@ int ttt_mlp_nc_bwd(const void* q, const void* k, const void* v, const float* w1,
                          {"dv", dv, tok(B, H, T, d), ib}, {"dw1", dw1, per_seq(B, H, 1LL * dh * d), 4},
                          {"dw2", dw2, per_seq(B, H, 1LL * d * dh), 4},
                          {"deta_tok", deta_tok, tok(B, H, T, 1), 4}});
+}
+
+size_t gated_linear_fwd_workspace_size(int B, int H, int T, int d, int io_dtype) {
+  if (B <= 0 || H <= 0 || T <= 0 || (d != 16 && d != 32 && d != 64)) return 0;
+  return ttt::gated_fwd_workspace_bytes(B, H, T, d, io_dtype == TTT_BF16);
+}
+
+size_t gated_linear_bwd_workspace_size(int B, int H, int T, int d, int gated, int io_dtype) {
+  if (B <= 0 || H <= 0 || T <= 0 || (d != 16 && d != 32 && d != 64)) return 0;
+  return ttt::gated_bwd_workspace_bytes(B, H, T, d, gated != 0, io_dtype == TTT_BF16);
+}
+
+int gated_linear_fwd(const void* q, const void* k, const void* v, const float* log_gate,
+                     const float* w0, long long w0_batch_stride, const int* lengths, void* z,
+                     float* w_out, int B, int H, int T, int d, float eta, const float* eta_tok,
+                     int io_dtype, void* workspace, size_t workspace_bytes, ttt_stream_t stream) {
+  const char* fn = "gated_linear_fwd";
+  int rc = check_gated(fn, {q, k, v, z}, {w0, w_out}, log_gate, lengths, B, H, T, d, eta, eta_tok, io_dtype);
+  if (rc != TTT_OK) return rc;
+  if (!w0) return fail(TTT_E_INVALID, "%s: w0 must be non-null", fn);
+  if (w0_batch_stride < 0 || w0_batch_stride % 4 != 0)
+    return fail(TTT_E_INVALID, "%s: w0_batch_stride must be a non-negative multiple of 4", fn);
+  rc = check_workspace(fn, workspace, workspace_bytes, gated_linear_fwd_workspace_size(B, H, T, d, io_dtype));
+  if (rc != TTT_OK) return rc;
+  ttt::GatedArgs a{q, k, v, log_gate, w0, w0_batch_stride, lengths, B, H, T, eta, eta_tok};
+  a.z = z;
+  a.w_out = w_out;
+  const hipError_t e = ttt::launch_gated_fwd(a, d, io_dtype == TTT_BF16, workspace, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(TTT_E_HIP, "%s launch: %s", fn, hipGetErrorString(e));
+  return finite_outputs(TTT_OK, fn, stream,
+                        {{"z", z, tok(B, H, T, d), io_bytes(io_dtype)}, {"w_out", w_out, per_seq(B, H, 1LL * d * d), 4}});
+}
+
+int gated_linear_bwd(const void* q, const void* k, const void* v, const float* log_gate,
+                     const float* w0, long long w0_batch_stride, const int* lengths,
+                     const void* dz, const float* dw_out, void* dq, void* dk, void* dv, float* dw0,
+                     float* dlog_gate, int B, int H, int T, int d, float eta, const float* eta_tok,
+                     float* deta_tok, int io_dtype, void* workspace, size_t workspace_bytes,
+                     ttt_stream_t stream) {
+  const char* fn = "gated_linear_bwd";
+  int rc = check_gated(fn, {q, k, v, dz, dq, dk, dv}, {w0, dw_out, dw0}, log_gate, lengths, B, H, T, d, eta,
+                       eta_tok, io_dtype);
+  if (rc != TTT_OK) return rc;
+  if (!w0 || !dw0) return fail(TTT_E_INVALID, "%s: w0 and dw0 must be non-null", fn);
+  if (w0_batch_stride < 0 || w0_batch_stride % 4 != 0)
+    return fail(TTT_E_INVALID, "%s: w0_batch_stride must be a non-negative multiple of 4", fn);
+  if (dlog_gate && !log_gate) return fail(TTT_E_INVALID, "%s: dlog_gate needs log_gate", fn);
+  if (deta_tok && !eta_tok) return fail(TTT_E_INVALID, "%s: deta_tok needs eta_tok", fn);
+  if (!all_aligned({dlog_gate, deta_tok}, 4))
+    return fail(TTT_E_INVALID, "%s: dlog_gate and deta_tok must be 4-byte aligned", fn);
+  rc = check_workspace(fn, workspace, workspace_bytes,
+                       gated_linear_bwd_workspace_size(B, H, T, d, dlog_gate != nullptr, io_dtype));
+  if (rc != TTT_OK) return rc;
+  ttt::GatedArgs a{q, k, v, log_gate, w0, w0_batch_stride, lengths, B, H, T, eta, eta_tok};
+  a.dz = dz;
+  a.dw_out = dw_out;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dw0 = dw0;
+  a.dgate = T > 0 ? dlog_gate : nullptr;
+  a.deta_tok = deta_tok;
+  const hipError_t e = ttt::launch_gated_bwd(a, d, io_dtype == TTT_BF16, workspace, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(TTT_E_HIP, "%s launch: %s", fn, hipGetErrorString(e));
+  const int ib = io_bytes(io_dtype);
+  return finite_outputs(TTT_OK, fn, stream,
+                        {{"dq", dq, tok(B, H, T, d), ib}, {"dk", dk, tok(B, H, T, d), ib},
+                         {"dv", dv, tok(B, H, T, d), ib}, {"dw0", dw0, per_seq(B, H, 1LL * d * d), 4},
+                         {"dlog_gate", dlog_gate, tok(B, H, T, 1), 4}, {"deta_tok", deta_tok, tok(B, H, T, 1), 4}});
+}
+
+int gated_linear_step(const void* q, const void* k, const void* v, const float* log_gate, float* w,
+                      void* z, int B, int H, int d, float eta, const float* eta_tok, int io_dtype,
+                      ttt_stream_t stream) {
+  const char* fn = "gated_linear_step";
+  const int rc = check_gated(fn, {q, k, v, z}, {w}, log_gate, nullptr, B, H, 1, d, eta, eta_tok, io_dtype);
+  if (rc != TTT_OK) return rc;
+  if (!w) return fail(TTT_E_INVALID, "%s: w must be non-null", fn);
+  ttt::GatedArgs a{q, k, v, log_gate, nullptr, 0, nullptr, B, H, 1, eta, eta_tok};
+  a.z = z;
+  const hipError_t e = ttt::launch_gated_step(a, w, d, io_dtype == TTT_BF16, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(TTT_E_HIP, "%s launch: %s", fn, hipGetErrorString(e));
+  return finite_outputs(TTT_OK, fn, stream,
+                        {{"z", z, tok(B, H, 1, d), io_bytes(io_dtype)}, {"w", w, per_seq(B, H, 1LL * d * d), 4}});
+}
+
+int token_norm_fwd(const void* x, const float* weight, const float* bias, const void* gate,
+                   const float* scale, const void* res, void* y, int B, int H, int T, int d, int kind,
+                   int act, float eps, int io_dtype, ttt_stream_t stream) {
+  const char* fn = "token_norm_fwd";
+  const int rc = check_norm(fn, x, y, B, H, T, d, kind, act, eps, io_dtype);
+  if (rc != TTT_OK) return rc;
+  if (!all_aligned({x, gate, res, y}, static_cast<uintptr_t>(io_bytes(io_dtype))) || !all_aligned({weight, bias, scale}, 4))
+    return fail(TTT_E_INVALID, "%s: a tensor is not aligned to its elements", fn);
+  if (T == 0) return TTT_OK;
+  const ttt::NormArgs a{x, weight, bias, gate, scale, res, y, B, H, T, d, kind, act, eps};
+  const hipError_t e = ttt::launch_token_norm_fwd(a, io_dtype == TTT_BF16, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(TTT_E_HIP, "%s launch: %s", fn, hipGetErrorString(e));
+  return finite_outputs(TTT_OK, fn, stream, {{"y", y, tok(B, H, T, d), io_bytes(io_dtype)}});
+}
+
+size_t token_norm_bwd_workspace_size(int B, int H, int T, int d) {
+  if (B <= 0 || H <= 0 || T < 0 || d <= 0 || d > ttt::kTokenNormMaxDim) return 0;
+  return ttt::token_norm_bwd_workspace_bytes(B, H, T, d);
+}
+
+int token_norm_bwd(const void* x, const float* weight, const float* bias, const void* gate,
+                   const float* scale, const void* dy, void* dx, float* dweight, float* dbias,
+                   void* dgate, float* dscale, int B, int H, int T, int d, int kind, int act, float eps,
+                   int io_dtype, void* workspace, size_t workspace_bytes, ttt_stream_t stream) {
+  const char* fn = "token_norm_bwd";
+  int rc = check_norm(fn, x, dx, B, H, T, d, kind, act, eps, io_dtype);
+  if (rc != TTT_OK) return rc;
+  if (T > 0 && !dy) return fail(TTT_E_INVALID, "%s: token tensors must be non-null", fn);
+  if (!all_aligned({x, gate, dy, dx, dgate}, static_cast<uintptr_t>(io_bytes(io_dtype))) ||
+      !all_aligned({weight, bias, scale, dweight, dbias, dscale}, 4))
+    return fail(TTT_E_INVALID, "%s: a tensor is not aligned to its elements", fn);
+  if ((dweight && !weight) || (dbias && !bias) || (dgate && !gate) || (dscale && !scale))
+    return fail(TTT_E_INVALID, "%s: a gradient is wanted of an input that is null", fn);
+  const bool sums = dweight || dbias || dscale;
+  rc = check_workspace(fn, workspace, workspace_bytes, sums ? token_norm_bwd_workspace_size(B, H, T, d) : 0);
+  if (rc != TTT_OK) return rc;
+  if (T == 0 && !sums) return TTT_OK;
+  ttt::NormArgs a{x, weight, bias, gate, scale, nullptr, nullptr, B, H, T, d, kind, act, eps};
+  a.dy = dy;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.dgate = dgate;
+  a.dscale = dscale;
+  const hipError_t e = ttt::launch_token_norm_bwd(a, io_dtype == TTT_BF16, workspace, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(TTT_E_HIP, "%s launch: %s", fn, hipGetErrorString(e));
+  const long long n = static_cast<long long>(H) * d;
+  const int ib = io_bytes(io_dtype);
+  return finite_outputs(TTT_OK, fn, stream,
+                        {{"dx", dx, tok(B, H, T, d), ib}, {"dgate", dgate, tok(B, H, T, d), ib},
+                         {"dweight", dweight, n, 4}, {"dbias", dbias, n, 4}, {"dscale", dscale, n, 4}});
 }
 
 }  // extern "C"

@@ -1,0 +1,414 @@
+"""The gated linear recurrence (gated_linear_fwd, _bwd, _step): the float64 form against autograd
+and differences and the C ABI's refusals on the CPU, the kernels against the float64 form on the
+GPU.  The bounds are derived in gated_util.py."""
+import ctypes
+
+import pytest
+import torch
+
+import test_sequence_layers_amd as ttt
+from tests.gated_util import assert_within, gated_bounds, gated_inputs, gated_reference
+
+FAKE = 0x1000  # 16-byte aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ttt.load_library()
+
+
+# ------------------------------------------------------------------------------------- CPU
+
+def _autograd(x):
+    """z, the final state and every gradient by autograd through a chunk-free float64 form."""
+    t = {n: x[n].double().requires_grad_() for n in ("q", "k", "v", "w0", "log_gate", "eta_tok")}
+    B, H, T, d = t["q"].shape
+    w = t["w0"].expand(B, H, d, d)
+    z = []
+    for i in range(T):
+        w = torch.exp(t["log_gate"][:, :, i, None, None]) * w + x["eta"] * t["eta_tok"][:, :, i, None, None] * (
+            t["v"][:, :, i, :, None] * t["k"][:, :, i, None, :])
+        z.append((w * t["q"][:, :, i, None, :]).sum(-1))
+    z = torch.stack(z, 2)
+    loss = (z * x["dz"].double()).sum() + (w * x["dw_out"].double()).sum()
+    grads = torch.autograd.grad(loss, list(t.values()))
+    return z, w, dict(zip(("dq", "dk", "dv", "dw0", "dlog_gate", "deta_tok"), grads))
+
+
+def test_reference_against_autograd():
+    x = gated_inputs(2, 2, 9, 4, "f32", "soft", rates=True, batch_w0=True, seed=1)
+    ref = gated_reference(x)
+    z, w, grads = _autograd(x)
+    assert torch.allclose(ref["z"], z, rtol=1e-12, atol=1e-12)
+    assert torch.allclose(ref["w_out"], w, rtol=1e-12, atol=1e-12)
+    for n, g in grads.items():
+        assert torch.allclose(ref[n], g, rtol=1e-11, atol=1e-11), n
+
+
+def test_reference_gradients_against_differences():
+    x = gated_inputs(1, 2, 7, 4, "f32", "soft", rates=True, batch_w0=True, seed=2)
+    ref = gated_reference(x)
+    loss = lambda y: sum(float((gated_reference(y, backward=False)[o] * y[u].double()).sum())
+                         for o, u in (("z", "dz"), ("w_out", "dw_out")))
+    h = 1e-5
+    for n in ("q", "k", "v", "w0", "log_gate", "eta_tok"):
+        step = torch.randn(x[n].shape, dtype=torch.float64, generator=torch.Generator().manual_seed(3))
+        up = loss({**x, n: x[n].double() + h * step}) - loss({**x, n: x[n].double() - h * step})
+        # central differences of a smooth function: error h^2 times third derivatives of size O(10)
+        assert abs(up / (2 * h) - float((ref["d" + n] * step).sum())) < 1e-6, n
+
+
+def test_a_gate_of_minus_infinity_starts_a_new_sequence():
+    x = gated_inputs(1, 1, 12, 4, "f32", "soft", seed=3)
+    x["log_gate"][..., 5] = -float("inf")
+    ref = gated_reference(x)
+    tail = {n: (t[:, :, 5:] if n in ("q", "k", "v", "dz", "log_gate") and t is not None else t) for n, t in x.items()}
+    tail["w0"] = torch.zeros_like(x["w0"])
+    part = gated_reference(tail)
+    assert torch.equal(ref["z"][:, :, 5:], part["z"]) and torch.equal(ref["dk"][:, :, 5:], part["dk"])
+    assert float(ref["dlog_gate"][0, 0, 5]) == 0.0
+
+
+def _call(lib, fn, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, gate=None, w0=FAKE, stride=0, lengths=None, z=FAKE, w_out=None, dz=FAKE,
+             dw_out=None, dq=FAKE, dk=FAKE, dv=FAKE, dw0=FAKE, dgate=None, B=1, H=1, T=16, d=16, eta=0.1,
+             eta_tok=None, deta=None, io=0, ws=FAKE, ws_bytes=1 << 30)
+    a.update(kw)
+    head = [a[n] for n in ("q", "k", "v", "gate", "w0", "stride", "lengths")]
+    if fn == "gated_linear_fwd":
+        return lib.gated_linear_fwd(*head, a["z"], a["w_out"], a["B"], a["H"], a["T"], a["d"], a["eta"],
+                                    a["eta_tok"], a["io"], a["ws"], a["ws_bytes"], None)
+    if fn == "gated_linear_bwd":
+        return lib.gated_linear_bwd(*head, a["dz"], a["dw_out"], a["dq"], a["dk"], a["dv"], a["dw0"], a["dgate"],
+                                    a["B"], a["H"], a["T"], a["d"], a["eta"], a["eta_tok"], a["deta"], a["io"],
+                                    a["ws"], a["ws_bytes"], None)
+    return lib.gated_linear_step(a["q"], a["k"], a["v"], a["gate"], a["w0"], a["z"], a["B"], a["H"], a["d"],
+                                 a["eta"], a["eta_tok"], a["io"], None)
+
+
+ALL = ("gated_linear_fwd", "gated_linear_bwd", "gated_linear_step")
+INVALID, UNSUPPORTED = -1, -2
+
+
+@pytest.mark.parametrize("fn", ALL)
+@pytest.mark.parametrize("bad, want", [
+    (dict(q=None), INVALID), (dict(v=None), INVALID), (dict(w0=None), INVALID), (dict(B=0), INVALID),
+    (dict(H=-1), INVALID), (dict(d=0), INVALID), (dict(eta=float("nan")), INVALID), (dict(eta=float("inf")), INVALID),
+    (dict(io=2), INVALID), (dict(k=FAKE + 8), INVALID), (dict(w0=FAKE + 4), INVALID), (dict(gate=FAKE + 2), INVALID),
+    (dict(eta_tok=FAKE + 1), INVALID), (dict(d=48), UNSUPPORTED), (dict(d=128), UNSUPPORTED),
+    (dict(B=1 << 20, H=1 << 20), INVALID)])
+def test_refusals(lib, fn, bad, want):
+    assert _call(lib, fn, **bad) == want
+    assert fn in ttt.last_error()
+
+
+@pytest.mark.parametrize("fn", ALL[:2])
+@pytest.mark.parametrize("bad, want", [
+    (dict(T=-1), INVALID), (dict(stride=-4), INVALID), (dict(stride=3), INVALID), (dict(lengths=FAKE + 2), INVALID),
+    (dict(B=1 << 15, H=1 << 14, T=1 << 20), UNSUPPORTED)])
+def test_refusals_of_sequences(lib, fn, bad, want):
+    assert _call(lib, fn, **bad) == want
+    assert fn in ttt.last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(dz=None), dict(dq=None), dict(dw0=None), dict(dgate=FAKE), dict(deta=FAKE),
+                                 dict(gate=FAKE, dgate=FAKE + 2), dict(dw0=FAKE + 8),
+                                 dict(gate=FAKE, dgate=FAKE, ws=None), dict(gate=FAKE, dgate=FAKE, ws_bytes=15),
+                                 dict(gate=FAKE, dgate=FAKE, ws=FAKE + 4)])
+def test_refusals_of_the_backward_pass(lib, bad):
+    assert _call(lib, "gated_linear_bwd", **bad) == INVALID
+    assert "gated_linear_bwd" in ttt.last_error()
+
+
+def test_workspace_sizes_of_bad_shapes_are_zero(lib):
+    for bad in ((0, 1, 16, 16), (1, 0, 16, 16), (1, 1, 0, 16), (1, 1, 16, 48)):
+        assert lib.gated_linear_fwd_workspace_size(*bad, 1) == 0
+        assert lib.gated_linear_bwd_workspace_size(*bad, 1, 1) == 0
+
+
+def test_bindings_refuse_cpu_tensors():
+    x = torch.zeros(1, 1, 4, 16)
+    with pytest.raises(ValueError):
+        ttt.gated_linear_fwd(x, x, x, torch.zeros(1, 16, 16), 0.1)
+    with pytest.raises(ValueError):
+        ttt.gated_linear_step(x[:, :, 0], x[:, :, 0], x[:, :, 0], torch.zeros(1, 1, 16, 16), 0.1)
+
+
+# ------------------------------------------------------------------------------------- GPU
+
+def _to_gpu(x, device="cuda"):
+    return {n: t.to(device) if torch.is_tensor(t) else t for n, t in x.items()}
+
+
+def _forward(g, **kw):
+    return ttt.gated_linear_fwd(g["q"], g["k"], g["v"], g["w0"], g["eta"], g["log_gate"], eta_tok=g["eta_tok"],
+                                lengths=g["lengths"], return_state=True, **kw)
+
+
+def _backward(g, with_dw_out=True, **kw):
+    got = ttt.gated_linear_bwd(g["q"], g["k"], g["v"], g["w0"], g["eta"], g["log_gate"], g["dz"],
+                               g["dw_out"] if with_dw_out else None, eta_tok=g["eta_tok"], lengths=g["lengths"], **kw)
+    names = ["dq", "dk", "dv", "dw0"] + ["dlog_gate"] * (g["log_gate"] is not None) + ["deta_tok"] * (g["eta_tok"] is not None)
+    assert len(got) == len(names)
+    return dict(zip(names, got))
+
+
+def _check(x, with_dw_out=True, backward=True):
+    print({n: (tuple(t.shape) if torch.is_tensor(t) else t) for n, t in x.items()}, x["q"].dtype, flush=True)
+    ref = gated_reference(x, with_dw_out, backward=backward)
+    tol = gated_bounds(x, ref, with_dw_out, backward)
+    g = _to_gpu(x)
+    z, w = _forward(g)
+    assert_within("z", z, ref["z"], tol["z"])
+    assert_within("w_out", w, ref["w_out"], tol["w_out"])
+    if backward:
+        for n, t in _backward(g, with_dw_out).items():
+            assert_within(n, t, ref[n], tol[n])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [16, 32, 64])
+@pytest.mark.parametrize("T", [1, 2, 16, 17, 63, 64, 65, 130, 300])
+def test_lengths(io, d, T):
+    _check(gated_inputs(2, 3, T, d, io, "soft", rates=True, seed=T + d))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", ["none", "zero", "strong", "grow", "resets", "lowest"])
+@pytest.mark.parametrize("d", [16, 64])
+def test_gates(io, gate, d):
+    _check(gated_inputs(1, 2, 200, d, io, gate, batch_w0=True, seed=5))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [16, 32, 64])
+def test_ragged_batch(io, d):
+    x = gated_inputs(6, 2, 150, d, io, "soft", rates=True, lengths=[0, 1, 64, 150, 99, 1000], seed=6)
+    # what lies past a row's end is not read
+    for b, n in enumerate([0, 1, 64, 150, 99, 150]):
+        for name in ("q", "k", "v", "dz"):
+            x[name][b, :, n:] = float("nan")
+        x["log_gate"][b, :, n:] = x["eta_tok"][b, :, n:] = float("nan")
+    clean = {n: torch.nan_to_num(t) if n in ("log_gate", "eta_tok") else t for n, t in x.items()}
+    clean = {n: torch.nan_to_num(t.float()).to(t.dtype) if n in ("q", "k", "v", "dz") else t for n, t in clean.items()}
+    clean["lengths"] = torch.clamp(x["lengths"], max=150)
+    ref = gated_reference(clean)
+    tol = gated_bounds(clean, ref)
+    g = _to_gpu(x)
+    z, w = _forward(g)
+    got = {"z": z, "w_out": w, **_backward(g)}
+    for n, t in got.items():
+        assert_within(n, t, ref[n], tol[n])
+    for n in ("z", "dq", "dk", "dv", "dlog_gate", "deta_tok"):
+        assert not got[n][0].any() and not got[n][1, :, 1:].any(), n
+
+
+@pytest.mark.gpu
+def test_without_upstream_state_gradient():
+    _check(gated_inputs(2, 2, 100, 32, "bf16", "soft", seed=7), with_dw_out=False)
+
+
+@pytest.mark.gpu
+def test_no_tokens():
+    x = _to_gpu(gated_inputs(2, 3, 0, 32, "bf16", "soft", rates=True, seed=8))
+    z, w = _forward(x)
+    assert z.shape == (2, 3, 0, 32) and torch.equal(w, x["w0"].expand(2, 3, 32, 32))
+    got = _backward(x)
+    assert torch.equal(got["dw0"], x["dw_out"]) and got["dlog_gate"].shape == (2, 3, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("BHT", [(1, 1, 5000), (1, 3, 2500), (40, 16, 70), (2, 300, 130)])
+def test_few_long_and_many_short_sequences(io, BHT):
+    _check(gated_inputs(*BHT, 16 if BHT[2] > 1000 else 32, io, "resets", rates=True, seed=9))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_long_sequences_of_wide_heads(io):
+    _check(gated_inputs(1, 2, 2100, 64, io, "soft", rates=True, seed=19))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_a_state_that_is_not_finite_is_dropped_by_the_gate(io):
+    x = gated_inputs(2, 2, 90, 64, io, "soft", rates=True, seed=10)
+    x["log_gate"][..., 0] = -float("inf")
+    want = gated_reference(x)
+    tol = gated_bounds(x, want)
+    x["w0"][:] = float("nan")
+    g = _to_gpu(x)
+    z, w = _forward(g)
+    for n, t in {"z": z, "w_out": w, **_backward(g)}.items():
+        assert_within(n, t, want[n], tol[n])
+    state = torch.full((2, 2, 64, 64), float("inf"), device="cuda")
+    z0 = ttt.gated_linear_step(*(g[n][:, :, 0].contiguous() for n in "qkv"), state, g["eta"],
+                               g["log_gate"][:, :, 0].contiguous(), eta_tok=g["eta_tok"][:, :, 0].contiguous())
+    assert_within("step z", z0, want["z"][:, :, 0], tol["z"][:, :, 0])
+    assert torch.isfinite(state).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [16, 32, 64])
+@pytest.mark.parametrize("BH", [(1, 1), (3, 5), (70, 9)])
+def test_single_tokens(io, d, BH):
+    """Token by token with the state in place, against the whole sequence."""
+    B, H = BH
+    x = gated_inputs(B, H, 4, d, io, "resets", rates=True, seed=11)
+    ref = gated_reference(x, backward=False)
+    tol = gated_bounds(x, ref, backward=False)
+    g = _to_gpu(x)
+    w = g["w0"].expand(B, H, d, d).contiguous()
+    for t in range(4):
+        at = lambda n: g[n][:, :, t].contiguous()
+        z = ttt.gated_linear_step(at("q"), at("k"), at("v"), w, g["eta"], at("log_gate"), eta_tok=at("eta_tok"))
+        assert_within(f"z[{t}]", z, ref["z"][:, :, t], tol["z"][:, :, t])
+    assert_within("w", w, ref["w_out"], tol["w_out"])
+    z = ttt.gated_linear_step(at("q"), at("k"), at("v"), w, g["eta"])  # neither gate nor rates
+    assert torch.isfinite(z.float()).all()
+
+
+@pytest.mark.gpu
+def test_state_carry_and_delta_rule_family():
+    """Two calls with the state carried over equal one; without a gate it is the dot-product loss."""
+    x = _to_gpu(gated_inputs(2, 2, 192, 64, "f32", "none", seed=12))
+    z, w = _forward(x)
+    half = lambda n, i: x[n][:, :, 96 * i:96 * (i + 1)].contiguous()
+    za, wa = ttt.gated_linear_fwd(half("q", 0), half("k", 0), half("v", 0), x["w0"], x["eta"], return_state=True)
+    zb, wb = ttt.gated_linear_fwd(half("q", 1), half("k", 1), half("v", 1), wa, x["eta"], return_state=True)
+    zd, wd = ttt.ttt_linear_fwd(x["q"], x["k"], x["v"], x["w0"], x["eta"], 1, loss="dot", return_state=True)
+    cpu = {n: t.cpu() if torch.is_tensor(t) else t for n, t in x.items()}
+    ref = gated_reference(cpu, backward=False)
+    tol = gated_bounds(cpu, ref, backward=False)
+    for n, t in (("z", z), ("z", torch.cat([za, zb], 2)), ("w_out", w), ("w_out", wb)):
+        assert_within(n, t, ref[n], tol[n])
+    # the other entry point steps token by token: 192 more roundings of a state
+    assert_within("dot loss z", zd, ref["z"], 2 * tol["z"])
+    assert_within("dot loss w", wd, ref["w_out"], 2 * tol["w_out"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_same_bits_every_time_and_on_another_stream(io):
+    x = _to_gpu(gated_inputs(3, 4, 700, 64, io, "resets", rates=True, seed=13))
+    z, w = _forward(x)
+    grads = _backward(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for kw in ({}, {"stream": side}, {"stream": side.cuda_stream}):
+        z2, w2 = _forward(x, **kw)
+        g2 = _backward(x, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(z, z2) and torch.equal(w, w2)
+        for n in grads:
+            assert torch.equal(grads[n], g2[n]), n
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    xs = [_to_gpu(gated_inputs(2, 3, 500, 64, "bf16", "soft", rates=True, seed=s)) for s in (14, 15)]
+    want = [(_forward(x), _backward(x)) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            got[i].append((_forward(xs[i], stream=s), _backward(xs[i], stream=s)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for (z, w), grads in got[i]:
+            assert torch.equal(z, want[i][0][0]) and torch.equal(w, want[i][0][1])
+            for n, t in grads.items():
+                assert torch.equal(t, want[i][1][n]), n
+
+
+@pytest.mark.gpu
+def test_captured_and_replayed():
+    """Forward, backward and a step in one graph, replayed on new inputs between eager calls."""
+    x = _to_gpu(gated_inputs(2, 3, 300, 64, "bf16", "soft", rates=True, seed=16))
+    new = _to_gpu(gated_inputs(2, 3, 300, 64, "bf16", "soft", rates=True, seed=17))
+    state = torch.zeros(2, 3, 64, 64, device="cuda")
+    tok = {n: x[n][:, :, 0].clone() for n in ("q", "k", "v", "log_gate", "eta_tok")}
+    run = lambda: (_forward(x), _backward(x), ttt.gated_linear_step(tok["q"], tok["k"], tok["v"], state, 0.5,
+                                                                    tok["log_gate"], eta_tok=tok["eta_tok"]))
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (z, w), grads, zs = run()
+    for i in range(4):
+        if i == 2:
+            for n, t in x.items():
+                if torch.is_tensor(t):
+                    t.copy_(new[n])
+        state.fill_(0.25 * i)
+        graph.replay()
+        torch.cuda.synchronize()
+        (z2, w2), g2 = _forward(x), _backward(x)
+        after = state.clone()
+        state.fill_(0.25 * i)
+        zs2 = ttt.gated_linear_step(tok["q"], tok["k"], tok["v"], state, 0.5, tok["log_gate"], eta_tok=tok["eta_tok"])
+        torch.cuda.synchronize()
+        assert torch.equal(z, z2) and torch.equal(w, w2) and torch.equal(zs, zs2) and torch.equal(after, state)
+        for n in grads:
+            assert torch.equal(grads[n], g2[n]), n
+
+
+@pytest.mark.gpu
+def test_gradients_against_differences_of_the_kernel():
+    """Central differences of the float32 forward kernel along random directions."""
+    x = gated_inputs(1, 2, 150, 32, "f32", "soft", rates=True, batch_w0=True, seed=18)
+    g = _to_gpu(x)
+    grads = _backward(g)
+
+    def loss(y):
+        z, w = _forward(y)
+        return float((z.double() * y["dz"].double()).sum() + (w.double() * y["dw_out"].double()).sum())
+
+    h = 2.0 ** -6
+    for n in ("q", "k", "v", "w0", "log_gate", "eta_tok"):
+        step = torch.randn(g[n].shape, device="cuda", generator=torch.Generator("cuda").manual_seed(4))
+        step = step / step.norm()
+        diff = (loss({**g, n: g[n] + h * step}) - loss({**g, n: g[n] - h * step})) / (2 * h)
+        # in q, k, v, w0 and the rates the loss is linear, in the gates its third derivative along a
+        # unit step is below the gradient's norm; rounding of the loss's terms adds under 1e-3 / h of them
+        scale = float(grads["d" + n].double().norm())
+        assert abs(diff - float((grads["d" + n].double() * step.double()).sum())) < 1e-2 * scale, n
+
+
+@pytest.mark.gpu
+def test_finite_check_names_the_output():
+    x = _to_gpu(gated_inputs(1, 1, 20, 16, "f32", "soft", seed=20))
+    x["v"][0, 0, 3, 2] = float("inf")
+    before = ttt.set_check_finite(True)
+    try:
+        with pytest.raises(ttt.TTTError, match="gated_linear_fwd: non-finite values in z"):
+            _forward(x)
+    finally:
+        ttt.set_check_finite(before)
+
+
+@pytest.mark.gpu
+def test_bindings_refuse():
+    x = _to_gpu(gated_inputs(2, 2, 8, 16, "bf16", "soft", rates=True, seed=21))
+    with pytest.raises(ValueError, match="log_gate"):
+        ttt.gated_linear_fwd(x["q"], x["k"], x["v"], x["w0"], 0.5, x["log_gate"].double())
+    with pytest.raises(ValueError, match="lengths"):
+        ttt.gated_linear_fwd(x["q"], x["k"], x["v"], x["w0"], 0.5, lengths=torch.ones(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="contiguous"):
+        ttt.gated_linear_fwd(x["q"].transpose(1, 2), x["k"], x["v"], x["w0"], 0.5)
+    with pytest.raises(ValueError, match="w0"):
+        ttt.gated_linear_bwd(x["q"], x["k"], x["v"], x["w0"][:1], 0.5, x["log_gate"], x["dz"])
+    with pytest.raises(ValueError, match="dz"):
+        ttt.gated_linear_bwd(x["q"], x["k"], x["v"], x["w0"], 0.5, x["log_gate"], x["dz"].float())
+    with pytest.raises(ttt.TTTError, match="workspace"):
+        ttt.gated_linear_bwd(x["q"], x["k"], x["v"], x["w0"], 0.5, x["log_gate"], x["dz"],
+                             workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    flat = torch.zeros(2 * 2 * 8 * 16 + 1, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ttt.TTTError, match="aligned"):
+        ttt.gated_linear_fwd(flat[1:].view(2, 2, 8, 16), x["k"], x["v"], x["w0"], 0.5)
