@@ -191,7 +191,12 @@ struct GatedArgs {
   float* dw0 = nullptr;
   float* dgate = nullptr;
   float* deta_tok = nullptr;
-  double* ws_end = nullptr;  // workspace of the gate's gradient
+  // segments of spc chunks per sequence; the rest is the workspace (gated_linear.hip)
+  int nseg = 1, spc = 1;
+  float* seg_w = nullptr;
+  float* seg_g = nullptr;
+  float* seg_decay = nullptr;
+  double* ws_end = nullptr;
   float* ws_tok = nullptr;
 };
 

@@ -1,157 +1,450 @@
-// Gated linear recurrence, forward and backward, on the float32 matrix cores: d in {16, 32, 64},
-// fp32 or bf16 I/O (formulas in gated_linear.hpp; backward below).  One workgroup of d / 16 waves
-// per (batch, head) sequence walks its chunks; the d x d state stays in registers, 16 columns a
-// wave, in the MFMA C layout, which serves as an operand of the next chunk's products as it is.
+// Gated linear recurrence, forward and backward (formulas in gated_linear.hpp; backward below):
+// d in {16, 32, 64}, fp32 or bf16 I/O, any T.
 //
-// Every product is a sum of 16 x 16 tiles C = A B by v_mfma_f32_16x16x4_f32.  Lane (g, r) holds
-// row r of A and column r of B for k = 4 g + e (e = 0..3) of each block of 16 k, and rows
-// 4 g + e of column r of C: a C tile is an operand whose k runs along its rows, with no exchange.
+// A sequence is cut into segments of whole chunks, one workgroup of d / 16 waves each.  When a
+// sequence has several, gl_sums_kernel forms what each adds to the state, gl_scan_kernel turns
+// that into the state at each segment's start, and the main kernel walks the segments' chunks.
+// The d x d state stays in registers, 16 columns a wave, in the MFMA C layout.
+//
+// Every product is a sum of 16 x 16 tiles C = A B.  Lane (g, r) of a wave holds row r of A and
+// column r of B at k = 4 g + e and k = 16 + 4 g + e (e = 0..3) of each block of 32 k, and rows
+// 4 g + e of column r of C.  So two C tiles are an operand whose k runs along their rows, with no
+// exchange between lanes: the state feeds the next chunk's products as it is.
+//
+//   float32 I/O:  v_mfma_f32_16x16x4_f32.
+//   bf16 I/O:     v_mfma_f32_16x16x32_bf16.  Products of inputs are exact.  Factors that are not
+//     inputs are split into bf16 parts, x = hi + mid + lo: two parts (2^-16 of a term) where the
+//     result is rounded to bf16, three (2^-24) where it is a float32 output or the state itself.
 #include "gated_linear.hpp"
 
 namespace ttt {
 namespace {
 
 constexpr int kC = kGlChunk;
-constexpr int kPC = kGlPitch;
 
-__device__ __forceinline__ void mma(gl_f4& c, const gl_f4& a, const gl_f4& b) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
-}
-// operand with k along the rows of a row-major LDS matrix: row r0 + r, k = k0 + 4 g + e
-__device__ __forceinline__ gl_f4 along(const float* m, int ld, int r0, int k0, int g, int r) {
-  return *reinterpret_cast<const gl_f4*>(m + (r0 + r) * ld + k0 + 4 * g);
-}
-// operand with k down the rows: k = k0 + 4 g + e, column c0 + r
-__device__ __forceinline__ gl_f4 down(const float* m, int ld, int k0, int c0, int g, int r) {
-  const float* p = m + (k0 + 4 * g) * ld + c0 + r;
-  return gl_f4{p[0], p[ld], p[2 * ld], p[3 * ld]};
-}
+typedef bf16 gl_b4 __attribute__((ext_vector_type(4)));
+typedef bf16 gl_b8 __attribute__((ext_vector_type(8)));
+typedef short gl_s4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ gl_f4 at4(const float* p, int i) { return *reinterpret_cast<const gl_f4*>(p + i); }
 __device__ __forceinline__ gl_f4 keep4(float f, const gl_f4& x) {
   return gl_f4{gl_keep(f, x[0]), gl_keep(f, x[1]), gl_keep(f, x[2]), gl_keep(f, x[3])};
 }
-__device__ __forceinline__ gl_f4 at4(const float* p, int i) { return *reinterpret_cast<const gl_f4*>(p + i); }
+__device__ __forceinline__ float dot4(const gl_f4& a, const gl_f4& b) {
+  return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
+}
+// over the four lanes (g) that share r
+__device__ __forceinline__ float over_g(float x) {
+  x += __shfl_xor(x, 16, 64);
+  return x + __shfl_xor(x, 32, 64);
+}
 
-// A token tile (kC x D) on its way from HBM to LDS as float32: each thread holds 16 elements.
-template <typename IO, int D>
-struct Tile {
-  static constexpr int kThreads = 4 * D;
-  static constexpr int kVec = static_cast<int>(sizeof(IO));       // 16-byte vectors per thread
-  static constexpr int kPerVec = 16 / static_cast<int>(sizeof(IO));
-  gl_u4 x[kVec];
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t src, int tid) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      x[i] = __builtin_amdgcn_raw_buffer_load_b128(src, (tid + i * kThreads) * 16, 0, 0);
+// Matrices in LDS hold a token (or a row of token pairs) per row.  Math<IO>: their element and
+// layout, and operands over 32 k (`Half`: over 16, when d = 16).
+template <typename IO> struct Math;
+
+template <>
+struct Math<float> {
+  typedef float Elem;
+  static constexpr int kPad = 4;       // row pitch = columns + kPad: 16-byte rows, spread over the banks
+  static constexpr int kPlanes = 1;    // matrices that hold one product's factor
+  struct Op { gl_f4 a, b; };
+  template <int N> struct Parts { Op x; };
+  template <bool Half> static __device__ __forceinline__ Op along(const float* row, int p, int g) {
+    const float* m = row + 32 * p + 4 * g;
+    return Op{at4(m, 0), Half ? gl_f4{0.0f, 0.0f, 0.0f, 0.0f} : at4(m, Half ? 0 : 16)};
   }
-  __device__ __forceinline__ void put(float* m, int tid) const {
+  static __device__ __forceinline__ gl_f4 down16(const float* m, int ld, int k0, int cb, int g, int r) {
+    const float* q = m + (k0 + 4 * g) * ld + 16 * cb + r;
+    return gl_f4{q[0], q[ld], q[2 * ld], q[3 * ld]};
+  }
+  template <int D> static __device__ __forceinline__ Op down(const float* m, int ld, int p, int cb, int g, int r) {
+    return Op{down16(m, ld, 32 * p, cb, g, r), down16(m, ld, 32 * p + 16, cb, g, r)};
+  }
+  template <bool Half> static __device__ __forceinline__ gl_f4 mma(const Op& a, const Op& b, gl_f4 c) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const int at = (tid + i * kThreads) * kPerVec;
-      float* p = m + (at / D) * (D + 4) + at % D;
-      if constexpr (sizeof(IO) == 4) {
-        *reinterpret_cast<gl_u4*>(p) = x[i];
-      } else {
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[e], b.a[e], c, 0, 0, 0);
+    if constexpr (!Half) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          gl_f4 y;
-          y[0] = __builtin_bit_cast(float, x[i][2 * j] << 16);
-          y[1] = __builtin_bit_cast(float, x[i][2 * j] & 0xFFFF0000u);
-          y[2] = __builtin_bit_cast(float, x[i][2 * j + 1] << 16);
-          y[3] = __builtin_bit_cast(float, x[i][2 * j + 1] & 0xFFFF0000u);
-          *reinterpret_cast<gl_f4*>(p + 4 * j) = y;
-        }
-      }
+      for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[e], b.b[e], c, 0, 0, 0);
     }
+    return c;
+  }
+  template <int N> static __device__ __forceinline__ Parts<N> split(const gl_f4& a, const gl_f4& b) { return Parts<N>{Op{a, b}}; }
+    // the parts as rows (A), as columns (B)
+  template <int N, bool Half> static __device__ __forceinline__ gl_f4 mma_rows(const Parts<N>& a, const Op& b, gl_f4 c) { return mma<Half>(a.x, b, c); }
+  template <int N, bool Half> static __device__ __forceinline__ gl_f4 mma_cols(const Op& a, const Parts<N>& b, gl_f4 c) { return mma<Half>(a, b.x, c); }
+  static __device__ __forceinline__ void widen(const Op& x, gl_f4* a, gl_f4* b) {
+    *a = x.a;
+    *b = x.b;
+  }
+  // the factor's columns 16 cb + 4 g .. + 3 of one row
+  static __device__ __forceinline__ void put(float* row, int, int cb, int g, const gl_f4& x) {
+    *reinterpret_cast<gl_f4*>(row + 16 * cb + 4 * g) = x;
+  }
+  static __device__ __forceinline__ gl_f4 mma_planes(const Op& a, const float* row, int, int p, int g, gl_f4 c) {
+    return mma<false>(a, along<false>(row, p, g), c);
+  }
+  template <int D> static __device__ __forceinline__ gl_f4 row4(const float* row, int cb, int g) { return at4(row, 16 * cb + 4 * g); }
+  static __device__ __forceinline__ void store4(const gl_f4& x, __amdgpu_buffer_rsrc_t dst, int elem) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(gl_u4, x), dst, elem * 4, 0, 0);
+  }
+  template <int D> static __device__ __forceinline__ void put_vec(float* m, int vec, const gl_u4& x) {
+    const int at = vec * 4;
+    *reinterpret_cast<gl_u4*>(m + (at / D) * (D + kPad) + at % D) = x;
   }
 };
 
-// four consecutive features of a token, rounded once to the I/O type
-template <typename IO>
-__device__ __forceinline__ void store4(const gl_f4& x, __amdgpu_buffer_rsrc_t dst, int elem) {
-  if constexpr (sizeof(IO) == 4) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(gl_u4, x), dst, elem * 4, 0, 0);
-  } else {
-    typedef bf16 bf4 __attribute__((ext_vector_type(4)));
-    const bf4 y = {from_f32<bf16>(x[0]), from_f32<bf16>(x[1]), from_f32<bf16>(x[2]), from_f32<bf16>(x[3])};
+template <>
+struct Math<bf16> {
+  typedef bf16 Elem;
+  static constexpr int kPad = 8;
+  static constexpr int kPlanes = 2;  // hi and lo
+  typedef gl_b8 Op;
+  template <int N> struct Parts { Op x[N]; };
+  // Column 32 p + 16 b + 4 g + e of a row is kept at 32 p + 8 g + 4 b + e, so that a lane's eight
+  // k of a block are one 16-byte read.
+  template <bool Half> static __device__ __forceinline__ Op along(const bf16* row, int p, int g) {
+    if constexpr (Half) {
+      const gl_b4 x = *reinterpret_cast<const gl_b4*>(row + 4 * g);
+      return __builtin_shufflevector(x, x, 0, 1, 2, 3, 0, 1, 2, 3);
+    }
+    return *reinterpret_cast<const gl_b8*>(row + 32 * p + 8 * g);
+  }
+  template <int D> static __device__ __forceinline__ int place(int cb, int g) {
+    return D == 16 ? 4 * g : 32 * (cb >> 1) + 8 * g + 4 * (cb & 1);
+  }
+  // Transposing LDS read: the 16 lanes of a group give the addresses of four rows' 16 columns
+  // (lane 4 i + j: row i, columns 4 j .. + 3) and receive one column of four rows each.
+  template <int D> static __device__ __forceinline__ gl_s4 down16(const bf16* m, int ld, int k0, int cb, int g, int r) {
+    const bf16* q = m + (k0 + 4 * g + (r >> 2)) * ld + place<D>(cb, r & 3);
+    typedef __attribute__((address_space(3))) gl_s4 lds_s4;
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)q);
+  }
+  template <int D> static __device__ __forceinline__ Op down(const bf16* m, int ld, int p, int cb, int g, int r) {
+    const gl_s4 a = down16<D>(m, ld, 32 * p, cb, g, r), b = down16<D>(m, ld, 32 * p + 16, cb, g, r);
+    return __builtin_bit_cast(gl_b8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  template <bool Half> static __device__ __forceinline__ gl_f4 mma(const Op& a, const Op& b, gl_f4 c) {
+    if constexpr (Half) {
+      const gl_b4 x = __builtin_shufflevector(a, a, 0, 1, 2, 3), y = __builtin_shufflevector(b, b, 0, 1, 2, 3);
+      return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(gl_s4, x), __builtin_bit_cast(gl_s4, y), c, 0, 0, 0);
+    }
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  template <int N> static __device__ __forceinline__ Parts<N> split(const gl_f4& a, const gl_f4& b) {
+    Parts<N> y;
+    float rest[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y.x[n][i] = static_cast<bf16>(rest[i]);
+        if (n + 1 < N) rest[i] -= static_cast<float>(y.x[n][i]);
+      }
+    }
+    return y;
+  }
+  // the parts as rows (A), as columns (B), small ones first
+  template <int N, bool Half> static __device__ __forceinline__ gl_f4 mma_rows(const Parts<N>& a, const Op& b, gl_f4 c) {
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) c = mma<Half>(a.x[n], b, c);
+    return c;
+  }
+  template <int N, bool Half> static __device__ __forceinline__ gl_f4 mma_cols(const Op& a, const Parts<N>& b, gl_f4 c) {
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) c = mma<Half>(a, b.x[n], c);
+    return c;
+  }
+  static __device__ __forceinline__ void widen(const Op& x, gl_f4* a, gl_f4* b) {
+    *a = gl_f4{static_cast<float>(x[0]), static_cast<float>(x[1]), static_cast<float>(x[2]), static_cast<float>(x[3])};
+    *b = gl_f4{static_cast<float>(x[4]), static_cast<float>(x[5]), static_cast<float>(x[6]), static_cast<float>(x[7])};
+  }
+  static __device__ __forceinline__ void put(bf16* row, int plane, int cb, int g, const gl_f4& x) {
+    gl_b4 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hi[i] = static_cast<bf16>(x[i]);
+      lo[i] = static_cast<bf16>(x[i] - static_cast<float>(hi[i]));
+    }
+    const int at = place<32>(cb, g);
+    *reinterpret_cast<gl_b4*>(row + at) = hi;
+    *reinterpret_cast<gl_b4*>(row + plane + at) = lo;
+  }
+  static __device__ __forceinline__ gl_f4 mma_planes(const Op& a, const bf16* row, int plane, int p, int g, gl_f4 c) {
+    c = mma<false>(a, along<false>(row + plane, p, g), c);
+    return mma<false>(a, along<false>(row, p, g), c);
+  }
+  template <int D> static __device__ __forceinline__ gl_f4 row4(const bf16* row, int cb, int g) {
+    const gl_b4 x = *reinterpret_cast<const gl_b4*>(row + place<D>(cb, g));
+    return gl_f4{static_cast<float>(x[0]), static_cast<float>(x[1]), static_cast<float>(x[2]), static_cast<float>(x[3])};
+  }
+  static __device__ __forceinline__ void store4(const gl_f4& x, __amdgpu_buffer_rsrc_t dst, int elem) {
+    const gl_b4 y = {from_f32<bf16>(x[0]), from_f32<bf16>(x[1]), from_f32<bf16>(x[2]), from_f32<bf16>(x[3])};
     __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(gl_u2, y), dst, elem * 2, 0, 0);
   }
-}
+  template <int D> static __device__ __forceinline__ void put_vec(bf16* m, int vec, const gl_u4& x) {
+    const int at = vec * 8, cb = (at % D) >> 4, g = (at >> 2) & 3;  // eight columns: g and g + 1 of a block of 16
+    bf16* row = m + (at / D) * (D + kPad);
+    *reinterpret_cast<gl_u2*>(row + place<D>(cb, g)) = gl_u2{x[0], x[1]};
+    *reinterpret_cast<gl_u2*>(row + place<D>(cb, g + 1)) = gl_u2{x[2], x[3]};
+  }
+};
+template <typename IO, int D>
+struct Shape {
+  typedef typename Math<IO>::Elem Elem;
+  static constexpr int kNW = D / 16;                           // waves
+  static constexpr int kNP = D / 32 > 0 ? D / 32 : 1;          // blocks of 32 features
+  static constexpr bool kHalf = D == 16;
+  static constexpr int kLd = D + Math<IO>::kPad;               // row pitch of a token tile
+  static constexpr int kTile = kC * kLd;
+  static constexpr int kLdP = kC + Math<IO>::kPad;             // row pitch of a factor of token pairs
+  static constexpr int kPlane = kC * kLdP;
+  static constexpr int kVec = static_cast<int>(sizeof(IO));    // 16-byte vectors of a tile per thread
+};
+
+// A token tile (kC x D) on its way from HBM to LDS.
+template <typename IO, int D>
+struct Tile {
+  gl_u4 x[sizeof(IO)];
+  __device__ __forceinline__ void load(const IO* base, int c0, int len, int tid) {
+    const __amdgpu_buffer_rsrc_t src = gl_span(base + static_cast<size_t>(c0) * D, min(kC, len - c0) * D * static_cast<int>(sizeof(IO)));
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(IO)); ++i)
+      x[i] = __builtin_amdgcn_raw_buffer_load_b128(src, (tid + i * 4 * D) * 16, 0, 0);
+  }
+  __device__ __forceinline__ void put(typename Math<IO>::Elem* m, int tid) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(IO)); ++i) Math<IO>::template put_vec<D>(m, tid + i * 4 * D, x[i]);
+  }
+};
 
 // One sequence's view of the arguments.
-template <typename IO>
 struct Seq {
-  size_t tok0;       // first element of its tokens
-  size_t row0;       // first token
-  int len;           // tokens that count
+  int chain;
+  size_t row0;  // first token
+  int len;      // tokens that count
   const float* gate;
   const float* rate;
 };
-template <typename IO>
-__device__ __forceinline__ Seq<IO> sequence(const GatedArgs& a, int chain, int D) {
-  Seq<IO> s;
+__device__ __forceinline__ Seq sequence(const GatedArgs& a, int chain) {
+  Seq s;
+  s.chain = chain;
   s.row0 = static_cast<size_t>(chain) * a.T;
-  s.tok0 = s.row0 * D;
   s.len = gl_length(a.lengths, chain / a.H, a.T);
   s.gate = a.gate ? a.gate + s.row0 : nullptr;
   s.rate = a.eta_tok ? a.eta_tok + s.row0 : nullptr;
   return s;
 }
-
 // the token's log decay and rate (0, 0 past the sequence)
 struct GateRate {
   float g, e;
+  __device__ __forceinline__ void load(const Seq& s, float eta, int t) {
+    const bool in = t < s.len;
+    g = in && s.gate ? s.gate[t] : 0.0f;
+    e = in ? (s.rate ? eta * s.rate[t] : eta) : 0.0f;
+  }
 };
-template <typename IO>
-__device__ __forceinline__ GateRate gate_rate(const Seq<IO>& s, float eta, int t) {
-  const bool in = t < s.len;
-  GateRate x;
-  x.g = in && s.gate ? s.gate[t] : 0.0f;
-  x.e = in ? (s.rate ? eta * s.rate[t] : eta) : 0.0f;
-  return x;
+__device__ __forceinline__ const float* initial_state(const GatedArgs& a, int chain, int dd) {
+  return a.w0 + (chain / a.H) * a.w0_batch_stride + static_cast<size_t>(chain % a.H) * dd;
 }
 
+
+// A state in registers.  Tile b of wave wv holds X[16 b + 4 g + e][16 wv + r] of the matrix X that
+// `rows` says is W (false: W^T, so that W's rows lie along the registers).
+template <int D, bool kTransposed>
+__device__ __forceinline__ void load_state(gl_f4* x, const float* w, int wv, int g, int r) {
+#pragma unroll
+  for (int b = 0; b < D / 16; ++b) {
+    if constexpr (kTransposed) {
+      x[b] = w ? at4(w, (16 * wv + r) * D + 16 * b + 4 * g) : gl_f4{0.0f, 0.0f, 0.0f, 0.0f};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[b][e] = w ? w[(16 * b + 4 * g + e) * D + 16 * wv + r] : 0.0f;
+    }
+  }
+}
 template <int D>
+__device__ __forceinline__ void store_state_transposed(const gl_f4* x, float* w, int wv, int g, int r) {
+#pragma unroll
+  for (int b = 0; b < D / 16; ++b) *reinterpret_cast<gl_f4*>(w + (16 * wv + r) * D + 16 * b + 4 * g) = x[b];
+}
+
+// x <- whole x + sum over the chunk's tokens s of a_s c_s b_s^T, a the rows of the tile A, b the
+// wave's 16 columns (k down the tokens), c_s = c[s] (c2[s]).
+template <typename IO, int D, int N>
+__device__ __forceinline__ void update_state(gl_f4* x, float whole, const typename Math<IO>::Elem* A,
+                                             const typename Math<IO>::Op* b, const float* c, const float* c2,
+                                             int g, int r) {
+  typedef Math<IO> M;
+#pragma unroll
+  for (int ab = 0; ab < D / 16; ++ab) x[ab] = keep4(whole, x[ab]);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    gl_f4 lo, hi;
+    M::widen(b[p], &lo, &hi);
+    lo *= at4(c, 32 * p + 4 * g);
+    hi *= at4(c, 32 * p + 16 + 4 * g);
+    if (c2) {
+      lo *= at4(c2, 32 * p + 4 * g);
+      hi *= at4(c2, 32 * p + 16 + 4 * g);
+    }
+    const typename M::template Parts<N> f = M::template split<N>(lo, hi);
+#pragma unroll
+    for (int ab = 0; ab < D / 16; ++ab)
+      x[ab] = M::template mma_cols<N, false>(M::template down<D>(A, Shape<IO, D>::kLd, p, ab, g, r), f, x[ab]);
+  }
+}
+// the state as an operand: parts over blocks of 32 rows
+template <typename IO, int D, int N>
+__device__ __forceinline__ void split_state(typename Math<IO>::template Parts<N>* y, const gl_f4* x) {
+#pragma unroll
+  for (int p = 0; p < Shape<IO, D>::kNP; ++p)
+    y[p] = Math<IO>::template split<N>(x[2 * p], Shape<IO, D>::kHalf ? gl_f4{0.0f, 0.0f, 0.0f, 0.0f} : x[Shape<IO, D>::kHalf ? 0 : 2 * p + 1]);
+}
+// rows of the state times a token's row: C[16 rows][16 tokens]
+template <typename IO, int D, int N>
+__device__ __forceinline__ gl_f4 state_times(const typename Math<IO>::template Parts<N>* w, const typename Math<IO>::Elem* row, int g) {
+  typedef Shape<IO, D> S;
+  gl_f4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int p = 0; p < S::kNP; ++p)
+    c = Math<IO>::template mma_rows<N, S::kHalf>(w[p], Math<IO>::template along<S::kHalf>(row, p, g), c);
+  return c;
+}
+// C[16 tokens of a][16 tokens of b]: products of rows
+template <typename IO, int D>
+__device__ __forceinline__ gl_f4 row_products(const typename Math<IO>::Elem* a, const typename Math<IO>::Elem* b, int g) {
+  typedef Shape<IO, D> S;
+  gl_f4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int p = 0; p < S::kNP; ++p)
+    c = Math<IO>::template mma<S::kHalf>(Math<IO>::template along<S::kHalf>(a, p, g), Math<IO>::template along<S::kHalf>(b, p, g), c);
+  return c;
+}
+
+// ---------------------------------------------------------------- segments
+//
+// What a segment adds to the state from zero.  Side 0: sum over its tokens s of (decay to the
+// segment's end) e_s v_s k_s^T, for the states.  Side 1 (backward): sum over its tokens u of
+// (decay from the segment's start) dz_u q_u^T, for the states' gradients.
+template <typename IO, int D>
+struct SumsLds {
+  typename Math<IO>::Elem a[Shape<IO, D>::kTile], b[Shape<IO, D>::kTile];
+  GlDecays dec;
+};
+
+template <typename IO, int D>
+__global__ __launch_bounds__(4 * D) void gl_sums_kernel(GatedArgs a) {
+  typedef Math<IO> M;
+  typedef Shape<IO, D> S;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+  SumsLds<IO, D>& L = *reinterpret_cast<SumsLds<IO, D>*>(lds_raw);
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int chain = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg, side = blockIdx.y;
+  // the last segment adds to no other's start, the first to no other's end
+  if (seg == (side == 0 ? a.nseg - 1 : 0)) return;
+  const Seq s = sequence(a, chain);
+  const IO* rows = static_cast<const IO*>(side == 0 ? a.k : a.q) + s.row0 * D;
+  const IO* cols = static_cast<const IO*>(side == 0 ? a.v : a.dz) + s.row0 * D;
+  const int nchunks = (a.T + kC - 1) / kC, first = seg * a.spc, n = min(a.spc, nchunks - first);
+  gl_f4 x[S::kNW];
+#pragma unroll
+  for (int i = 0; i < S::kNW; ++i) x[i] = gl_f4{0.0f, 0.0f, 0.0f, 0.0f};
+  Tile<IO, D> ta, tb;
+  GateRate gr;
+  float all = 1.0f;
+  auto chunk = [&](int i) { return side == 0 ? first + i : first + n - 1 - i; };
+  auto prefetch = [&](int c) {
+    ta.load(rows, c * kC, s.len, tid);
+    tb.load(cols, c * kC, s.len, tid);
+    if (wv == 0) gr.load(s, a.eta, c * kC + lane);
+  };
+  prefetch(chunk(0));
+  for (int i = 0; i < n; ++i) {
+    gl_barrier();  // the previous chunk's tiles have been read
+    ta.put(L.a, tid);
+    tb.put(L.b, tid);
+    if (wv == 0) gl_decays(gr.g, gr.e, &L.dec, lane);
+    gl_barrier();
+    if (i + 1 < n) prefetch(chunk(i + 1));
+    typename M::Op b[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) b[p] = M::template down<D>(L.b, S::kLd, p, wv, g, r);
+    const float whole = L.dec.whole[0];
+    all *= whole;
+    update_state<IO, D, 3>(x, whole, L.a, b, side == 0 ? L.dec.to : L.dec.from, side == 0 ? L.dec.e : nullptr, g, r);
+  }
+  float* out = (side == 0 ? a.seg_w : a.seg_g) + static_cast<size_t>(blockIdx.x) * D * D;
+  store_state_transposed<D>(x, out, wv, g, r);
+  if (tid == 0) a.seg_decay[static_cast<size_t>(side) * a.B * a.H * a.nseg + blockIdx.x] = all;
+}
+
+// The sums become the states at the segments' starts (side 0, first to last from w0) and the
+// gradients at their ends (side 1, last to first from dw_out), in place.
+template <int D>
+__global__ __launch_bounds__(256) void gl_scan_kernel(GatedArgs a) {
+  constexpr int kPer = D * D / 4;  // threads per sequence
+  const long long item = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const int chain = static_cast<int>(item / kPer), at = static_cast<int>(item % kPer) * 4, side = blockIdx.y;
+  if (chain >= a.B * a.H) return;
+  const size_t seg0 = static_cast<size_t>(chain) * a.nseg;
+  float* x = (side == 0 ? a.seg_w : a.seg_g) + seg0 * D * D + at;
+  const float* decay = a.seg_decay + static_cast<size_t>(side) * a.B * a.H * a.nseg + seg0;
+  gl_f4 state = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (side == 0) state = at4(initial_state(a, chain, D * D), at);
+  else if (a.dw_out) state = at4(a.dw_out + static_cast<size_t>(chain) * D * D, at);
+  for (int i = 0; i < a.nseg; ++i) {
+    const int m = side == 0 ? i : a.nseg - 1 - i;
+    float* p = x + static_cast<size_t>(m) * D * D;
+    if (i + 1 < a.nseg) {
+      const gl_f4 sum = at4(p, 0);
+      *reinterpret_cast<gl_f4*>(p) = state;
+      state = keep4(decay[m], state) + sum;
+    } else {
+      *reinterpret_cast<gl_f4*>(p) = state;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- forward
+template <typename IO, int D>
 struct FwdLds {
-  float q[kC * (D + 4)], k[kC * (D + 4)], v[kC * (D + 4)];
-  float p[kC * kPC];
+  typename Math<IO>::Elem q[Shape<IO, D>::kTile], k[Shape<IO, D>::kTile], v[Shape<IO, D>::kTile];
+  typename Math<IO>::Elem p[Math<IO>::kPlanes * Shape<IO, D>::kPlane];
   GlDecays dec;
 };
 
 template <typename IO, int D>
 __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
-  constexpr int NW = D / 16, PD = D + 4;
+  typedef Math<IO> M;
+  typedef Shape<IO, D> S;
+  constexpr int NW = S::kNW, LD = S::kLd, LDP = S::kLdP;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
-  FwdLds<D>& L = *reinterpret_cast<FwdLds<D>*>(lds_raw);
+  FwdLds<IO, D>& L = *reinterpret_cast<FwdLds<IO, D>*>(lds_raw);
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int chain = blockIdx.x, T = a.T;
-  const Seq<IO> s = sequence<IO>(a, chain, D);
-  const IO* q = static_cast<const IO*>(a.q) + s.tok0;
-  const IO* k = static_cast<const IO*>(a.k) + s.tok0;
-  const IO* v = static_cast<const IO*>(a.v) + s.tok0;
-  IO* z = static_cast<IO*>(a.z) + s.tok0;
-  const int nchunks = (T + kC - 1) / kC;
+  const int chain = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg, T = a.T;
+  const Seq s = sequence(a, chain);
+  const IO* q = static_cast<const IO*>(a.q) + s.row0 * D;
+  const IO* k = static_cast<const IO*>(a.k) + s.row0 * D;
+  const IO* v = static_cast<const IO*>(a.v) + s.row0 * D;
+  IO* z = static_cast<IO*>(a.z) + s.row0 * D;
+  const int nchunks = (T + kC - 1) / kC, first = seg * a.spc, end = min(nchunks, first + a.spc);
 
-  // W^T, columns j of the wave: tile ib holds W[16 wv + r][16 ib + 4 g + e]
-  gl_f4 w[NW];
-  const float* w0 = a.w0 + (chain / a.H) * a.w0_batch_stride + static_cast<size_t>(chain % a.H) * D * D;
-  const size_t at_w = static_cast<size_t>(16 * wv + r) * D + 4 * g;
-#pragma unroll
-  for (int ib = 0; ib < NW; ++ib) w[ib] = *reinterpret_cast<const gl_f4*>(w0 + at_w + 16 * ib);
-
+  gl_f4 w[NW];  // W^T: W's rows 16 wv + r
+  load_state<D, true>(w, a.nseg > 1 ? a.seg_w + static_cast<size_t>(blockIdx.x) * D * D : initial_state(a, chain, D * D), wv, g, r);
   Tile<IO, D> tq, tk, tv;
   GateRate gr;
   auto prefetch = [&](int c) {
-    const int c0 = c * kC, bytes = min(kC, s.len - c0) * D * static_cast<int>(sizeof(IO));
-    const size_t off = static_cast<size_t>(c0) * D;
-    tq.load(gl_span(q + off, bytes), tid);
-    tk.load(gl_span(k + off, bytes), tid);
-    tv.load(gl_span(v + off, bytes), tid);
-    if (wv == 0) gr = gate_rate(s, a.eta, c0 + lane);
+    tq.load(q, c * kC, s.len, tid);
+    tk.load(k, c * kC, s.len, tid);
+    tv.load(v, c * kC, s.len, tid);
+    if (wv == 0) gr.load(s, a.eta, c * kC + lane);
   };
-  if (nchunks > 0) prefetch(0);
-  for (int c = 0; c < nchunks; ++c) {
+  if (first < end) prefetch(first);
+  for (int c = first; c < end; ++c) {
     const int c0 = c * kC;
     gl_barrier();  // the previous chunk's tiles have been read
     tq.put(L.q, tid);
@@ -159,7 +452,7 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
     tv.put(L.v, tid);
     if (wv == 0) gl_decays(gr.g, gr.e, &L.dec, lane);
     gl_barrier();
-    if (c + 1 < nchunks) prefetch(c + 1);
+    if (c + 1 < end) prefetch(c + 1);
 
     // P[u][s] = exp(b_u - b_s) e_s (q_u . k_s) for s <= u, the wave's blocks of 16 tokens u
 #pragma unroll
@@ -168,50 +461,38 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
       const float uh = L.dec.bh[u], ul = L.dec.bl[u];
 #pragma unroll
       for (int st = 0; st < 4; ++st) {
-        if (st > ut) break;
-        gl_f4 p = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int kb = 0; kb < NW; ++kb) mma(p, along(L.k, PD, 16 * st, 16 * kb, g, r), along(L.q, PD, 16 * ut, 16 * kb, g, r));
+        if (st > (ut | 1)) break;  // up to the end of the block of 32
         const int s4 = 16 * st + 4 * g;
-        const gl_f4 sh = at4(L.dec.bh, s4), sl = at4(L.dec.bl, s4), e = at4(L.dec.e, s4);
+        gl_f4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (st <= ut) {
+          p = row_products<IO, D>(L.k + (16 * st + r) * LD, L.q + u * LD, g);
+          const gl_f4 sh = at4(L.dec.bh, s4), sl = at4(L.dec.bl, s4), e = at4(L.dec.e, s4);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) p[x] = s4 + x <= u ? p[x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
-        *reinterpret_cast<gl_f4*>(&L.p[u * kPC + s4]) = p;
+          for (int x = 0; x < 4; ++x) p[x] = s4 + x <= u ? p[x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
+        }
+        M::put(L.p + u * LDP, S::kPlane, st, g, p);
       }
     }
     gl_barrier();
 
-    gl_f4 vf[4];  // V, k down the tokens, the wave's features
+    typename M::Op vf[2];  // V, k down the tokens, the wave's features
 #pragma unroll
-    for (int st = 0; st < 4; ++st) vf[st] = down(L.v, PD, 16 * st, 16 * wv, g, r);
-    const int rows = min(kC, T - c0);
-    const __amdgpu_buffer_rsrc_t dst = gl_span(z + static_cast<size_t>(c0) * D, rows * D * static_cast<int>(sizeof(IO)));
+    for (int p = 0; p < 2; ++p) vf[p] = M::template down<D>(L.v, LD, p, wv, g, r);
+    typename M::template Parts<2> wp[S::kNP];
+    split_state<IO, D, 2>(wp, w);
+    const __amdgpu_buffer_rsrc_t dst = gl_span(z + static_cast<size_t>(c0) * D, min(kC, T - c0) * D * static_cast<int>(sizeof(IO)));
 #pragma unroll
     for (int ut = 0; ut < 4; ++ut) {  // Z^T: rows j, columns u
-      gl_f4 zi = {0.0f, 0.0f, 0.0f, 0.0f}, zp = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int ib = 0; ib < NW; ++ib) mma(zi, w[ib], along(L.q, PD, 16 * ut, 16 * ib, g, r));
-#pragma unroll
-      for (int st = 0; st <= ut; ++st) mma(zp, vf[st], along(L.p, kPC, 16 * ut, 16 * st, g, r));
       const int u = 16 * ut + r;
-      const float f = L.dec.from[u];
-      store4<IO>(zp + keep4(f, zi), dst, u * D + 16 * wv + 4 * g);
+      const gl_f4 zi = state_times<IO, D, 2>(wp, L.q + u * LD, g);
+      gl_f4 zp = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int p = 0; p <= ut / 2; ++p) zp = M::mma_planes(vf[p], L.p + u * LDP, S::kPlane, p, g, zp);
+      M::store4(zp + keep4(L.dec.from[u], zi), dst, u * D + 16 * wv + 4 * g);
     }
-    const float whole = L.dec.whole[0];
-#pragma unroll
-    for (int st = 0; st < 4; ++st) vf[st] *= at4(L.dec.to, 16 * st + 4 * g) * at4(L.dec.e, 16 * st + 4 * g);
-#pragma unroll
-    for (int ib = 0; ib < NW; ++ib) {
-      w[ib] = keep4(whole, w[ib]);
-#pragma unroll
-      for (int st = 0; st < 4; ++st) mma(w[ib], down(L.k, PD, 16 * st, 16 * ib, g, r), vf[st]);
-    }
+    update_state<IO, D, 3>(w, L.dec.whole[0], L.k, vf, L.dec.to, L.dec.e, g, r);
   }
-  if (a.w_out) {
-    float* wo = a.w_out + static_cast<size_t>(chain) * D * D + at_w;
-#pragma unroll
-    for (int ib = 0; ib < NW; ++ib) *reinterpret_cast<gl_f4*>(wo + 16 * ib) = w[ib];
-  }
+  if (a.w_out && seg == a.nseg - 1) store_state_transposed<D>(w, a.w_out + static_cast<size_t>(chain) * D * D, wv, g, r);
 }
 
 // ---------------------------------------------------------------- backward
@@ -222,7 +503,7 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
 //   dk_s = e_s (sum_{u >= s} exp(b_u - b_s) (dz_u . v_s) q_u + exp(b_C - b_s) G^T v_s),
 //   de_s = v_s . x_s,
 // W the state before the chunk, G the gradient at its end.  Two roles share no data: one
-// workgroup walks a sequence forward with W for dq, another walks it backward with G for dk and
+// workgroup walks a segment forward with W for dq, another walks it backward with G for dk and
 // dv.  So no state is stored on the way.
 //
 // dg_t = a_t <G_t, W_{t-1}> is the sum over the pairs (s, u), s < t <= u, of what token s
@@ -231,46 +512,53 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
 //   row_u = sum_{s < u} m_us, col_s = sum_{u > s} m_us (pairs inside the chunk),
 //   in_u = exp(b_u) dz_u . W q_u,  out_s = exp(b_C - b_s) e_s v_s . G k_s,  past = exp(b_C) <G, W>.
 // Only the row - col sums cancel, over one chunk; nothing grows with the sequence.  `past` follows
-// from <G, W> at the sequence's end: past_c = <G, W>_end(c) - sum out, <G, W>_start(c) = past_c +
+// from <G, W> at the segment's end: past_c = <G, W>_end(c) - sum out, <G, W>_start(c) = past_c +
 // sum in.  The two roles store row, in, col, out per token, and gl_dgate_kernel adds them.
-template <int D>
+template <typename IO, int D>
 struct BwdLds {
-  float q[kC * (D + 4)], k[kC * (D + 4)], v[kC * (D + 4)], z[kC * (D + 4)];
-  float p[kC * kPC], r[kC * kPC];
-  float part[D / 16][kC];
+  typedef Shape<IO, D> S;
+  typename S::Elem q[S::kTile], k[S::kTile], v[S::kTile], z[S::kTile];
+  typename S::Elem p[Math<IO>::kPlanes * S::kPlane], r[Math<IO>::kPlanes * S::kPlane];
+  float part[S::kNW][kC];
   GlDecays dec;
 };
 
 template <typename IO, int D>
 __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
-  constexpr int NW = D / 16, PD = D + 4;
+  typedef Math<IO> M;
+  typedef Shape<IO, D> S;
+  constexpr int NW = S::kNW, LD = S::kLd, LDP = S::kLdP;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
-  BwdLds<D>& L = *reinterpret_cast<BwdLds<D>*>(lds_raw);
+  BwdLds<IO, D>& L = *reinterpret_cast<BwdLds<IO, D>*>(lds_raw);
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int chain = blockIdx.x >> 1, role = blockIdx.x & 1, T = a.T;
-  const Seq<IO> s = sequence<IO>(a, chain, D);
-  const IO* q = static_cast<const IO*>(a.q) + s.tok0;
-  const IO* k = static_cast<const IO*>(a.k) + s.tok0;
-  const IO* v = static_cast<const IO*>(a.v) + s.tok0;
-  const IO* dz = static_cast<const IO*>(a.dz) + s.tok0;
-  const int nchunks = (T + kC - 1) / kC;
+  // the two roles of a segment are 8 workgroups apart: the same XCD, so one L2 serves both
+  const int item = (blockIdx.x >> 4) * 8 + (blockIdx.x & 7), role = (blockIdx.x >> 3) & 1;
+  if (item >= a.B * a.H * a.nseg) return;
+  const int chain = item / a.nseg, seg = item % a.nseg, T = a.T;
+  const Seq s = sequence(a, chain);
+  const IO* q = static_cast<const IO*>(a.q) + s.row0 * D;
+  const IO* k = static_cast<const IO*>(a.k) + s.row0 * D;
+  const IO* v = static_cast<const IO*>(a.v) + s.row0 * D;
+  const IO* dz = static_cast<const IO*>(a.dz) + s.row0 * D;
+  const int nchunks = (T + kC - 1) / kC, first = seg * a.spc, end = min(nchunks, first + a.spc);
   const size_t rows_all = static_cast<size_t>(a.B) * a.H * T;
   float* row_o = a.ws_tok ? a.ws_tok + s.row0 : nullptr;
   float* in_o = a.ws_tok ? row_o + rows_all : nullptr;
   float* col_o = a.ws_tok ? in_o + rows_all : nullptr;
   float* out_o = a.ws_tok ? col_o + rows_all : nullptr;
+  // the gradient of the state at the segment's end
+  const float* g_end = a.nseg > 1 ? a.seg_g + static_cast<size_t>(item) * D * D
+                                  : a.dw_out ? a.dw_out + static_cast<size_t>(chain) * D * D : nullptr;
 
   Tile<IO, D> tq, tk, tv, tz;
   GateRate gr;
   auto prefetch = [&](int c) {
-    const int c0 = c * kC, bytes = min(kC, s.len - c0) * D * static_cast<int>(sizeof(IO));
-    const size_t off = static_cast<size_t>(c0) * D;
-    tq.load(gl_span(q + off, bytes), tid);
-    tk.load(gl_span(k + off, bytes), tid);
-    tv.load(gl_span(v + off, bytes), tid);
-    tz.load(gl_span(dz + off, bytes), tid);
-    if (wv == 0) gr = gate_rate(s, a.eta, c0 + lane);
+    tq.load(q, c * kC, s.len, tid);
+    tk.load(k, c * kC, s.len, tid);
+    tv.load(v, c * kC, s.len, tid);
+    tz.load(dz, c * kC, s.len, tid);
+    if (wv == 0) gr.load(s, a.eta, c * kC + lane);
   };
   auto stage = [&]() {
     tq.put(L.q, tid);
@@ -279,28 +567,18 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
     tz.put(L.z, tid);
     if (wv == 0) gl_decays(gr.g, gr.e, &L.dec, lane);
   };
-  // over the four lanes (g) that share a token r
-  auto over_g = [](float x) {
-    x += __shfl_xor(x, 16, 64);
-    return x + __shfl_xor(x, 32, 64);
-  };
 
   if (role == 0) {
-    // W, columns i of the wave: tile jb holds W[16 jb + 4 g + e][16 wv + r]
-    gl_f4 w[NW];
-    const float* w0 = a.w0 + (chain / a.H) * a.w0_batch_stride + static_cast<size_t>(chain % a.H) * D * D;
-#pragma unroll
-    for (int jb = 0; jb < NW; ++jb)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[jb][e] = w0[(16 * jb + 4 * g + e) * D + 16 * wv + r];
-    IO* dq = static_cast<IO*>(a.dq) + s.tok0;
-    if (nchunks > 0) prefetch(0);
-    for (int c = 0; c < nchunks; ++c) {
+    gl_f4 w[NW];  // W's columns 16 wv + r
+    load_state<D, false>(w, a.nseg > 1 ? a.seg_w + static_cast<size_t>(item) * D * D : initial_state(a, chain, D * D), wv, g, r);
+    IO* dq = static_cast<IO*>(a.dq) + s.row0 * D;
+    if (first < end) prefetch(first);
+    for (int c = first; c < end; ++c) {
       const int c0 = c * kC;
       gl_barrier();
       stage();
       gl_barrier();
-      if (c + 1 < nchunks) prefetch(c + 1);
+      if (c + 1 < end) prefetch(c + 1);
 #pragma unroll
       for (int it = 0; it < 4 / NW; ++it) {
         const int ut = wv + it * NW, u = 16 * ut + r;
@@ -308,21 +586,21 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
         float row = 0.0f;
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
-          if (st > ut) break;
-          gl_f4 rd = {0.0f, 0.0f, 0.0f, 0.0f}, p = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int kb = 0; kb < NW; ++kb) mma(rd, along(L.v, PD, 16 * st, 16 * kb, g, r), along(L.z, PD, 16 * ut, 16 * kb, g, r));
+          if (st > (ut | 1)) break;
           const int s4 = 16 * st + 4 * g;
-          const gl_f4 sh = at4(L.dec.bh, s4), sl = at4(L.dec.bl, s4), e = at4(L.dec.e, s4);
+          gl_f4 rd = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (st <= ut) {
+            rd = row_products<IO, D>(L.v + (16 * st + r) * LD, L.z + u * LD, g);
+            const gl_f4 sh = at4(L.dec.bh, s4), sl = at4(L.dec.bl, s4), e = at4(L.dec.e, s4);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) rd[x] = s4 + x <= u ? rd[x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
-          *reinterpret_cast<gl_f4*>(&L.r[u * kPC + s4]) = rd;
-          if (row_o) {
+            for (int x = 0; x < 4; ++x) rd[x] = s4 + x <= u ? rd[x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
+            if (row_o) {
+              const gl_f4 p = row_products<IO, D>(L.k + (16 * st + r) * LD, L.q + u * LD, g);
 #pragma unroll
-            for (int kb = 0; kb < NW; ++kb) mma(p, along(L.k, PD, 16 * st, 16 * kb, g, r), along(L.q, PD, 16 * ut, 16 * kb, g, r));
-#pragma unroll
-            for (int x = 0; x < 4; ++x) row += s4 + x < u ? p[x] * rd[x] : 0.0f;
+              for (int x = 0; x < 4; ++x) row += s4 + x < u ? p[x] * rd[x] : 0.0f;
+            }
           }
+          M::put(L.r + u * LDP, S::kPlane, st, g, rd);
         }
         if (row_o) {
           row = over_g(row);
@@ -330,36 +608,26 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
         }
       }
       gl_barrier();
-      gl_f4 kf[4];
+      typename M::Op kf[2];
 #pragma unroll
-      for (int st = 0; st < 4; ++st) kf[st] = down(L.k, PD, 16 * st, 16 * wv, g, r);
+      for (int p = 0; p < 2; ++p) kf[p] = M::template down<D>(L.k, LD, p, wv, g, r);
+      typename M::template Parts<3> wp[S::kNP];
+      split_state<IO, D, 3>(wp, w);
       const __amdgpu_buffer_rsrc_t dst = gl_span(dq + static_cast<size_t>(c0) * D, min(kC, T - c0) * D * static_cast<int>(sizeof(IO)));
 #pragma unroll
       for (int ut = 0; ut < 4; ++ut) {
-        gl_f4 xi = {0.0f, 0.0f, 0.0f, 0.0f}, xp = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int jb = 0; jb < NW; ++jb) mma(xi, w[jb], along(L.z, PD, 16 * ut, 16 * jb, g, r));
-#pragma unroll
-        for (int st = 0; st <= ut; ++st) mma(xp, kf[st], along(L.r, kPC, 16 * ut, 16 * st, g, r));
         const int u = 16 * ut + r;
-        const float f = L.dec.from[u];
-        xi = keep4(f, xi);
+        const gl_f4 xi = keep4(L.dec.from[u], state_times<IO, D, 3>(wp, L.z + u * LD, g));
+        gl_f4 xp = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int p = 0; p <= ut / 2; ++p) xp = M::mma_planes(kf[p], L.r + u * LDP, S::kPlane, p, g, xp);
         if (row_o) {
-          const gl_f4 qu = along(L.q, PD, 16 * ut, 16 * wv, g, r);
-          float in = over_g(qu[0] * xi[0] + qu[1] * xi[1] + qu[2] * xi[2] + qu[3] * xi[3]);
+          const float in = over_g(dot4(M::template row4<D>(L.q + u * LD, wv, g), xi));
           if (g == 0) L.part[wv][u] = in;
         }
-        store4<IO>(xi + xp, dst, u * D + 16 * wv + 4 * g);
+        M::store4(xi + xp, dst, u * D + 16 * wv + 4 * g);
       }
-      const float whole = L.dec.whole[0];
-#pragma unroll
-      for (int st = 0; st < 4; ++st) kf[st] *= at4(L.dec.to, 16 * st + 4 * g) * at4(L.dec.e, 16 * st + 4 * g);
-#pragma unroll
-      for (int jb = 0; jb < NW; ++jb) {
-        w[jb] = keep4(whole, w[jb]);
-#pragma unroll
-        for (int st = 0; st < 4; ++st) mma(w[jb], down(L.v, PD, 16 * st, 16 * jb, g, r), kf[st]);
-      }
+      update_state<IO, D, 3>(w, L.dec.whole[0], L.v, kf, L.dec.to, L.dec.e, g, r);
       if (row_o) {
         gl_barrier();
         if (wv == 0 && c0 + lane < T) {
@@ -370,41 +638,32 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
         }
       }
     }
-    if (row_o) {  // <dL/dW, W> at the sequence's end
+    if (row_o) {  // <G, W> at the segment's end
       double x = 0.0;
-      if (a.dw_out) {
-        const float* dw = a.dw_out + static_cast<size_t>(chain) * D * D;
+      if (g_end) {
 #pragma unroll
-        for (int jb = 0; jb < NW; ++jb)
+        for (int b = 0; b < NW; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x += static_cast<double>(w[jb][e]) * dw[(16 * jb + 4 * g + e) * D + 16 * wv + r];
+          for (int e = 0; e < 4; ++e) x += static_cast<double>(w[b][e]) * g_end[(16 * b + 4 * g + e) * D + 16 * wv + r];
       }
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
-      if (lane == 0) a.ws_end[static_cast<size_t>(chain) * NW + wv] = x;
+      if (lane == 0) a.ws_end[static_cast<size_t>(item) * NW + wv] = x;
     }
   } else {
-    // G twice: gt holds G[16 wv + r][16 ib + 4 g + e] (k along i), gn holds G[16 jb + 4 g + e][16 wv + r]
-    gl_f4 gt[NW], gn[NW];
-    const float* dw = a.dw_out ? a.dw_out + static_cast<size_t>(chain) * D * D : nullptr;
-    const size_t at_w = static_cast<size_t>(16 * wv + r) * D + 4 * g;
-#pragma unroll
-    for (int ib = 0; ib < NW; ++ib)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        gt[ib][e] = dw ? dw[at_w + 16 * ib + e] : 0.0f;
-        gn[ib][e] = dw ? dw[(16 * ib + 4 * g + e) * D + 16 * wv + r] : 0.0f;
-      }
-    IO* dk = static_cast<IO*>(a.dk) + s.tok0;
-    IO* dv = static_cast<IO*>(a.dv) + s.tok0;
+    gl_f4 gt[NW], gn[NW];  // G twice: its rows 16 wv + r, its columns 16 wv + r
+    load_state<D, true>(gt, g_end, wv, g, r);
+    load_state<D, false>(gn, g_end, wv, g, r);
+    IO* dk = static_cast<IO*>(a.dk) + s.row0 * D;
+    IO* dv = static_cast<IO*>(a.dv) + s.row0 * D;
     float* de_o = a.deta_tok ? a.deta_tok + s.row0 : nullptr;
-    if (nchunks > 0) prefetch(nchunks - 1);
-    for (int c = nchunks - 1; c >= 0; --c) {
+    if (first < end) prefetch(end - 1);
+    for (int c = end - 1; c >= first; --c) {
       const int c0 = c * kC;
       gl_barrier();
       stage();
       gl_barrier();
-      if (c > 0) prefetch(c - 1);
+      if (c > first) prefetch(c - 1);
       // the wave's blocks of 16 tokens s: rows of P^T and R^T (decayed, without e_s)
       float diag[4 / NW], col[4 / NW];
 #pragma unroll
@@ -414,74 +673,63 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
         float cs = 0.0f, dg = 0.0f;
 #pragma unroll
         for (int ut = 0; ut < 4; ++ut) {
-          if (ut < st) continue;
-          gl_f4 p = {0.0f, 0.0f, 0.0f, 0.0f}, rd = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (ut < (st & ~1)) continue;  // from the start of the block of 32
+          gl_f4 p = {0.0f, 0.0f, 0.0f, 0.0f}, rd = p;
+          if (ut >= st) {
+            p = row_products<IO, D>(L.q + (16 * ut + r) * LD, L.k + ss * LD, g);
+            rd = row_products<IO, D>(L.z + (16 * ut + r) * LD, L.v + ss * LD, g);
+            const int u4 = 16 * ut + 4 * g;
+            const gl_f4 uh = at4(L.dec.bh, u4), ul = at4(L.dec.bl, u4);
 #pragma unroll
-          for (int kb = 0; kb < NW; ++kb) {
-            mma(p, along(L.q, PD, 16 * ut, 16 * kb, g, r), along(L.k, PD, 16 * st, 16 * kb, g, r));
-            mma(rd, along(L.z, PD, 16 * ut, 16 * kb, g, r), along(L.v, PD, 16 * st, 16 * kb, g, r));
+            for (int x = 0; x < 4; ++x) {
+              const float dec = gl_between(uh[x], ul[x], sh, sl);
+              const float m = p[x] * rd[x] * dec;
+              p[x] = u4 + x >= ss ? p[x] * dec : 0.0f;
+              rd[x] = u4 + x >= ss ? rd[x] * dec : 0.0f;
+              cs += u4 + x > ss ? m : 0.0f;
+              dg += u4 + x == ss ? m : 0.0f;
+            }
           }
-          const int u4 = 16 * ut + 4 * g;
-          const gl_f4 uh = at4(L.dec.bh, u4), ul = at4(L.dec.bl, u4);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float dec = u4 + x >= ss ? gl_between(uh[x], ul[x], sh, sl) : 0.0f;
-            const float m = u4 + x >= ss ? p[x] * rd[x] * dec : 0.0f;
-            p[x] = u4 + x >= ss ? p[x] * dec : 0.0f;
-            rd[x] = u4 + x >= ss ? rd[x] * dec : 0.0f;
-            cs += u4 + x > ss ? m : 0.0f;
-            dg += u4 + x == ss ? m : 0.0f;
-          }
-          *reinterpret_cast<gl_f4*>(&L.p[ss * kPC + u4]) = p;
-          *reinterpret_cast<gl_f4*>(&L.r[ss * kPC + u4]) = rd;
+          M::put(L.p + ss * LDP, S::kPlane, ut, g, p);
+          M::put(L.r + ss * LDP, S::kPlane, ut, g, rd);
         }
         col[it] = over_g(cs);
         diag[it] = over_g(dg);
       }
       gl_barrier();
-      gl_f4 zf[4], qf[4];  // dZ and Q, k down the tokens u, the wave's features
+      typename M::Op zf[2], qf[2];  // dZ and Q, k down the tokens u, the wave's features
 #pragma unroll
-      for (int ut = 0; ut < 4; ++ut) {
-        zf[ut] = down(L.z, PD, 16 * ut, 16 * wv, g, r);
-        qf[ut] = down(L.q, PD, 16 * ut, 16 * wv, g, r);
+      for (int p = 0; p < 2; ++p) {
+        zf[p] = M::template down<D>(L.z, LD, p, wv, g, r);
+        qf[p] = M::template down<D>(L.q, LD, p, wv, g, r);
       }
+      typename M::template Parts<3> tp[S::kNP];
+      typename M::template Parts<2> np[S::kNP];
+      split_state<IO, D, 3>(tp, gt);
+      split_state<IO, D, 2>(np, gn);
       const int bytes = min(kC, T - c0) * D * static_cast<int>(sizeof(IO));
       const __amdgpu_buffer_rsrc_t dstv = gl_span(dv + static_cast<size_t>(c0) * D, bytes);
       const __amdgpu_buffer_rsrc_t dstk = gl_span(dk + static_cast<size_t>(c0) * D, bytes);
 #pragma unroll
       for (int st = 0; st < 4; ++st) {
-        gl_f4 vi = {0.0f, 0.0f, 0.0f, 0.0f}, vp = vi, ki = vi, kp = vi;
-#pragma unroll
-        for (int ib = 0; ib < NW; ++ib) {
-          mma(vi, gt[ib], along(L.k, PD, 16 * st, 16 * ib, g, r));
-          mma(ki, gn[ib], along(L.v, PD, 16 * st, 16 * ib, g, r));
-        }
-#pragma unroll
-        for (int ut = st; ut < 4; ++ut) {
-          mma(vp, zf[ut], along(L.p, kPC, 16 * st, 16 * ut, g, r));
-          mma(kp, qf[ut], along(L.r, kPC, 16 * st, 16 * ut, g, r));
-        }
         const int ss = 16 * st + r;
         const float f = L.dec.to[ss], e = L.dec.e[ss];
-        vi = keep4(f, vi);
-        const gl_f4 vs = along(L.v, PD, 16 * st, 16 * wv, g, r);
-        const float out = over_g(vs[0] * vi[0] + vs[1] * vi[1] + vs[2] * vi[2] + vs[3] * vi[3]);
+        const gl_f4 vi = keep4(f, state_times<IO, D, 3>(tp, L.k + ss * LD, g));
+        const gl_f4 ki = keep4(f, state_times<IO, D, 2>(np, L.v + ss * LD, g));
+        gl_f4 vp = {0.0f, 0.0f, 0.0f, 0.0f}, kp = vp;
+#pragma unroll
+        for (int p = st / 2; p < 2; ++p) {
+          vp = M::mma_planes(zf[p], L.p + ss * LDP, S::kPlane, p, g, vp);
+          kp = M::mma_planes(qf[p], L.r + ss * LDP, S::kPlane, p, g, kp);
+        }
+        const float out = over_g(dot4(M::template row4<D>(L.v + ss * LD, wv, g), vi));
         if (g == 0) L.part[wv][ss] = out;
-        store4<IO>(e * (vi + vp), dstv, ss * D + 16 * wv + 4 * g);
-        store4<IO>(e * (keep4(f, ki) + kp), dstk, ss * D + 16 * wv + 4 * g);
+        M::store4(e * (vi + vp), dstv, ss * D + 16 * wv + 4 * g);
+        M::store4(e * (ki + kp), dstk, ss * D + 16 * wv + 4 * g);
       }
       const float whole = L.dec.whole[0];
-#pragma unroll
-      for (int ib = 0; ib < NW; ++ib) {
-        gt[ib] = keep4(whole, gt[ib]);
-        gn[ib] = keep4(whole, gn[ib]);
-#pragma unroll
-        for (int ut = 0; ut < 4; ++ut) {
-          const gl_f4 f = at4(L.dec.from, 16 * ut + 4 * g);
-          mma(gt[ib], down(L.q, PD, 16 * ut, 16 * ib, g, r), zf[ut] * f);
-          mma(gn[ib], down(L.z, PD, 16 * ut, 16 * ib, g, r), qf[ut] * f);
-        }
-      }
+      update_state<IO, D, 3>(gt, whole, L.q, zf, L.dec.from, nullptr, g, r);
+      update_state<IO, D, 2>(gn, whole, L.z, qf, L.dec.from, nullptr, g, r);
       gl_barrier();
 #pragma unroll
       for (int it = 0; it < 4 / NW; ++it) {
@@ -499,29 +747,29 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
         }
       }
     }
-    float* dw0 = a.dw0 + static_cast<size_t>(chain) * D * D + at_w;
-#pragma unroll
-    for (int ib = 0; ib < NW; ++ib) *reinterpret_cast<gl_f4*>(dw0 + 16 * ib) = gt[ib];
+    if (seg == 0) store_state_transposed<D>(gt, a.dw0 + static_cast<size_t>(chain) * D * D, wv, g, r);
   }
 }
 
 // dlog_gate from the per-token sums (see above): one wave per chunk, lane = token.  Each wave
-// first walks the sums of the later chunks of its sequence.
+// first walks the sums of the later chunks of its segment.
 __global__ __launch_bounds__(256) void gl_dgate_kernel(GatedArgs a, int nend) {
   const int lane = threadIdx.x & 63;
   const int nchunks = (a.T + kC - 1) / kC;
   const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (item >= static_cast<long long>(a.B) * a.H * nchunks) return;
-  const int chain = static_cast<int>(item / nchunks), c = static_cast<int>(item % nchunks);
+  const int chain = static_cast<int>(item / nchunks), c = static_cast<int>(item % nchunks), seg = c / a.spc;
   const size_t all = static_cast<size_t>(a.B) * a.H * a.T, row0 = static_cast<size_t>(chain) * a.T;
   const float* row = a.ws_tok + row0;
   const float* in = row + all;
   const float* col = in + all;
   const float* out = col + all;
   const int len = gl_length(a.lengths, chain / a.H, a.T);
-  double later = 0.0;  // over the tokens of later chunks
-  for (int t = (c + 1) * kC + lane; t < a.T; t += 64) later += static_cast<double>(in[t]) - out[t];
-  for (int x = lane; x < nend; x += 64) later += a.ws_end[static_cast<size_t>(chain) * nend + x];
+  const long long seg_end = static_cast<long long>(seg + 1) * a.spc * kC;
+  const int stop = seg_end < a.T ? static_cast<int>(seg_end) : a.T;
+  double later = 0.0;  // over the tokens of later chunks, and <G, W> at the segment's end
+  for (int t = (c + 1) * kC + lane; t < stop; t += 64) later += static_cast<double>(in[t]) - out[t];
+  if (lane < nend) later += a.ws_end[(static_cast<size_t>(chain) * a.nseg + seg) * nend + lane];
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) later += __shfl_xor(later, o, 64);
   const int t = c * kC + lane;
@@ -542,23 +790,61 @@ __global__ __launch_bounds__(256) void gl_dgate_kernel(GatedArgs a, int nend) {
   a.dgate[row0 + t] = live ? static_cast<float>(suf + (pre - o_t) + past) : 0.0f;
 }
 
+// ---------------------------------------------------------------- host
+
+// Chunks per segment.
+int chunks_per_segment(long long chains, int nchunks, int want) {
+  const long long segs = (want + chains - 1) / chains;  // workgroups wanted
+  const long long n = segs < 1 ? 1 : segs;
+  const long long spc = (nchunks + n - 1) / n;
+  return spc < 1 ? 1 : static_cast<int>(spc);
+}
+void plan(GatedArgs* a, bool bwd) {
+  const int nchunks = (a->T + kC - 1) / kC;
+  a->spc = chunks_per_segment(static_cast<long long>(a->B) * a->H, nchunks, bwd ? 512 : 512);
+  a->nseg = nchunks > 0 ? (nchunks + a->spc - 1) / a->spc : 1;
+}
+
+template <typename F>
+hipError_t allow_lds(F fn, int bytes) {
+  return bytes <= 64 * 1024 ? hipSuccess
+                            : hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename IO, int D>
+hipError_t segment_states(const GatedArgs& a, int sides, hipStream_t s) {
+  if (a.nseg == 1) return hipSuccess;
+  const int chains = a.B * a.H;
+  constexpr int bytes = sizeof(SumsLds<IO, D>);
+  const auto fn = gl_sums_kernel<IO, D>;
+  hipError_t e = allow_lds(fn, bytes);
+  if (e != hipSuccess) return e;
+  fn<<<dim3(chains * a.nseg, sides), dim3(4 * D), bytes, s>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  gl_scan_kernel<D><<<dim3(static_cast<unsigned>((static_cast<long long>(chains) * (D * D / 4) + 255) / 256), sides), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <typename IO, int D>
 hipError_t fwd(const GatedArgs& a, hipStream_t s) {
   const auto fn = gl_fwd_kernel<IO, D>;
-  constexpr int bytes = sizeof(FwdLds<D>);
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr int bytes = sizeof(FwdLds<IO, D>);
+  hipError_t e = allow_lds(fn, bytes);
+  if (e == hipSuccess) e = segment_states<IO, D>(a, 1, s);
   if (e != hipSuccess) return e;
-  fn<<<dim3(a.B * a.H), dim3(4 * D), bytes, s>>>(a);
+  fn<<<dim3(a.B * a.H * a.nseg), dim3(4 * D), bytes, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename IO, int D>
 hipError_t bwd(const GatedArgs& a, hipStream_t s) {
   const auto fn = gl_bwd_kernel<IO, D>;
-  constexpr int bytes = sizeof(BwdLds<D>);
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr int bytes = sizeof(BwdLds<IO, D>);
+  hipError_t e = allow_lds(fn, bytes);
+  if (e == hipSuccess) e = segment_states<IO, D>(a, 2, s);
   if (e != hipSuccess) return e;
-  fn<<<dim3(2 * a.B * a.H), dim3(4 * D), bytes, s>>>(a);
+  fn<<<dim3(16 * ((a.B * a.H * a.nseg + 7) / 8)), dim3(4 * D), bytes, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess || !a.dgate || a.T == 0) return e;
   const long long items = static_cast<long long>(a.B) * a.H * ((a.T + kC - 1) / kC);
@@ -566,26 +852,54 @@ hipError_t bwd(const GatedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-}  // namespace
-
-size_t gated_fwd_workspace_bytes(int, int, int, int, bool) { return 0; }
-
-size_t gated_bwd_workspace_bytes(int B, int H, int T, int d, bool gated, bool) {
-  if (!gated) return 0;
-  const size_t chains = static_cast<size_t>(B) * H;
-  return chains * (d / 16) * sizeof(double) + chains * T * 4 * sizeof(float);
+// The workspace: [ends, doubles][state sums][gradient sums][decays][per-token sums], each part
+// only where the call needs it; every part but the last is a multiple of 16 bytes.
+size_t carve(GatedArgs* a, int d, bool bwd, bool gated, void* ws) {
+  plan(a, bwd);
+  const size_t segs = static_cast<size_t>(a->B) * a->H * a->nseg, dd = static_cast<size_t>(d) * d;
+  unsigned char* p = static_cast<unsigned char*>(ws);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    unsigned char* q = p ? p + at : nullptr;
+    at += (bytes + 15) / 16 * 16;
+    return q;
+  };
+  if (gated) a->ws_end = reinterpret_cast<double*>(take(segs * (d / 16) * sizeof(double)));
+  if (a->nseg > 1) {
+    a->seg_w = reinterpret_cast<float*>(take(segs * dd * sizeof(float)));
+    if (bwd) a->seg_g = reinterpret_cast<float*>(take(segs * dd * sizeof(float)));
+    a->seg_decay = reinterpret_cast<float*>(take(2 * segs * sizeof(float)));
+  }
+  if (gated) a->ws_tok = reinterpret_cast<float*>(take(static_cast<size_t>(a->B) * a->H * a->T * 4 * sizeof(float)));
+  return at;
 }
 
-hipError_t launch_gated_fwd(GatedArgs a, int d, bool bf16_io, void*, hipStream_t s) {
+}  // namespace
+
+size_t gated_fwd_workspace_bytes(int B, int H, int T, int d, bool) {
+  GatedArgs a{};
+  a.B = B;
+  a.H = H;
+  a.T = T;
+  return carve(&a, d, false, false, nullptr);
+}
+
+size_t gated_bwd_workspace_bytes(int B, int H, int T, int d, bool gated, bool) {
+  GatedArgs a{};
+  a.B = B;
+  a.H = H;
+  a.T = T;
+  return carve(&a, d, true, gated, nullptr);
+}
+
+hipError_t launch_gated_fwd(GatedArgs a, int d, bool bf16_io, void* ws, hipStream_t s) {
+  carve(&a, d, false, false, ws);
   if (bf16_io) return d == 16 ? fwd<bf16, 16>(a, s) : d == 32 ? fwd<bf16, 32>(a, s) : fwd<bf16, 64>(a, s);
   return d == 16 ? fwd<float, 16>(a, s) : d == 32 ? fwd<float, 32>(a, s) : fwd<float, 64>(a, s);
 }
 
 hipError_t launch_gated_bwd(GatedArgs a, int d, bool bf16_io, void* ws, hipStream_t s) {
-  if (a.dgate) {
-    a.ws_end = static_cast<double*>(ws);
-    a.ws_tok = reinterpret_cast<float*>(a.ws_end + static_cast<size_t>(a.B) * a.H * (d / 16));
-  }
+  carve(&a, d, true, a.dgate != nullptr, ws);
   if (bf16_io) return d == 16 ? bwd<bf16, 16>(a, s) : d == 32 ? bwd<bf16, 32>(a, s) : bwd<bf16, 64>(a, s);
   return d == 16 ? bwd<float, 16>(a, s) : d == 32 ? bwd<float, 32>(a, s) : bwd<float, 64>(a, s);
 }
