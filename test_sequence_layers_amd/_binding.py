@@ -6,6 +6,7 @@ fallback; if the library is missing every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -628,24 +629,29 @@ def ttt_mlp_ln_fwd(q, k, v, w1, w2, ln_weight, ln_bias, eta, chunk, causal=True,
 
 # ------------------------------------------------------- gated linear recurrence, token norm
 
-def _on_stream(device, stream):
-    """Context in which torch allocates for the call's stream: outputs and workspaces taken
-    in it are reused in that stream's order."""
+_HERE = contextlib.nullcontext()
+
+
+def _enter(device, stream):
+    """(stream pointer, context) of a call: in the context torch allocates for the call's stream,
+    so that outputs and workspaces are reused in that stream's order, and the call's device is
+    the current one.  On the current stream of the current device there is nothing to enter."""
     torch = _torch()
     if stream is None:
         stream = torch.cuda.current_stream(device)
+        if device.index == torch.cuda.current_device():
+            return stream.cuda_stream, _HERE
     elif not hasattr(stream, "cuda_stream"):
         stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
                   else torch.cuda.default_stream(device))
-    return torch.cuda.stream(stream)
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _optional(t, shape, dtype, device, name):
     """Pointer of an optional contiguous tensor (None -> NULL)."""
     if t is None:
         return None
-    torch = _torch()
-    if (not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype
+    if (not isinstance(t, _torch().Tensor) or t.shape != shape or t.dtype != dtype
             or t.device != device or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t.data_ptr()
@@ -683,14 +689,15 @@ def gated_linear_fwd(q, k, v, w0, eta, log_gate=None, *, eta_tok=None, lengths=N
     gate = _optional(log_gate, (B, H, T), torch.float32, dev, "log_gate")
     rate = _rates(eta_tok, B, H, T, dev)
     lens = _optional(lengths, (B,), torch.int32, dev, "lengths")
-    with torch.cuda.device(dev), _on_stream(dev, stream):
+    on, here = _enter(dev, stream)
+    with here:
         z = _out(z, (B, H, T, d), q.dtype, dev, "z")
         if return_state or w_out is not None:
             w_out = _out(w_out, (B, H, d, d), torch.float32, dev, "w_out")
         ws, nbytes = _workspace(workspace, lib.gated_linear_fwd_workspace_size(B, H, T, d, io), dev)
         rc = lib.gated_linear_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate, w0.data_ptr(), stride,
                                   lens, z.data_ptr(), _pointer(w_out), B, H, T, d, float(eta), rate, io,
-                                  _pointer(ws), nbytes, _stream(dev, None))
+                                  _pointer(ws), nbytes, on)
     _check(rc)
     return (z, w_out) if w_out is not None else z
 
@@ -711,7 +718,8 @@ def gated_linear_bwd(q, k, v, w0, eta, log_gate, dz, dw_out=None, *, eta_tok=Non
     gate = _optional(log_gate, (B, H, T), torch.float32, dev, "log_gate")
     rate = _rates(eta_tok, B, H, T, dev)
     lens = _optional(lengths, (B,), torch.int32, dev, "lengths")
-    with torch.cuda.device(dev), _on_stream(dev, stream):
+    on, here = _enter(dev, stream)
+    with here:
         out = [torch.empty_like(q), torch.empty_like(q), torch.empty_like(q),
                torch.empty((B, H, d, d), dtype=torch.float32, device=dev)]
         per_token = lambda x: torch.empty((B, H, T), dtype=torch.float32, device=dev) if x is not None else None
@@ -721,7 +729,7 @@ def gated_linear_bwd(q, k, v, w0, eta, log_gate, dz, dw_out=None, *, eta_tok=Non
         rc = lib.gated_linear_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate, w0.data_ptr(), stride,
                                   lens, dz.data_ptr(), dw, *(x.data_ptr() for x in out), _pointer(dgate),
                                   B, H, T, d, float(eta), rate, _pointer(deta), io, _pointer(ws), nbytes,
-                                  _stream(dev, None))
+                                  on)
     _check(rc)
     return tuple(out + [x for x in (dgate, deta) if x is not None])
 
@@ -742,10 +750,11 @@ def gated_linear_step(q, k, v, w, eta, log_gate=None, *, eta_tok=None, z=None, s
     state = _optional(w, (B, H, d, d), torch.float32, dev, "w")
     gate = _optional(log_gate, (B, H), torch.float32, dev, "log_gate")
     rate = _optional(eta_tok, (B, H), torch.float32, dev, "eta_tok")
-    with torch.cuda.device(dev), _on_stream(dev, stream):
+    on, here = _enter(dev, stream)
+    with here:
         z = _out(z, (B, H, d), q.dtype, dev, "z")
         rc = lib.gated_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate, state, z.data_ptr(),
-                                   B, H, d, float(eta), rate, io, _stream(dev, None))
+                                   B, H, d, float(eta), rate, io, on)
     _check(rc)
     return z
 
@@ -789,10 +798,11 @@ def token_norm_fwd(x, kind, eps=1e-6, *, weight=None, bias=None, gate=None, act=
     par = [_optional(t, (H, d), torch.float32, dev, n)
            for t, n in ((weight, "weight"), (bias, "bias"), (scale, "scale"))]
     gp, rp = (_optional(t, x.shape, x.dtype, dev, n) for t, n in ((gate, "gate"), (res, "res")))
-    with torch.cuda.device(dev), _on_stream(dev, stream):
+    on, here = _enter(dev, stream)
+    with here:
         y = _out(y, x.shape, x.dtype, dev, "y")
         rc = lib.token_norm_fwd(x.data_ptr(), par[0], par[1], gp, par[2], rp, y.data_ptr(), B, H, T, d,
-                                _NORMS[kind], _ACTS[act], float(eps), io, _stream(dev, None))
+                                _NORMS[kind], _ACTS[act], float(eps), io, on)
     _check(rc)
     return y
 
@@ -811,7 +821,8 @@ def token_norm_bwd(x, dy, kind, eps=1e-6, *, weight=None, bias=None, gate=None, 
     named = ((weight, "weight"), (bias, "bias"), (scale, "scale"))
     par = [_optional(t, (H, d), torch.float32, dev, n) for t, n in named]
     gp = _optional(gate, x.shape, x.dtype, dev, "gate")
-    with torch.cuda.device(dev), _on_stream(dev, stream):
+    on, here = _enter(dev, stream)
+    with here:
         dx = torch.empty_like(x)
         dpar = [torch.empty((H, d), dtype=torch.float32, device=dev) if t is not None else None
                 for t, _ in named]
@@ -821,7 +832,7 @@ def token_norm_bwd(x, dy, kind, eps=1e-6, *, weight=None, bias=None, gate=None, 
         rc = lib.token_norm_bwd(x.data_ptr(), par[0], par[1], gp, par[2], dyp, dx.data_ptr(),
                                 _pointer(dpar[0]), _pointer(dpar[1]), _pointer(dg), _pointer(dpar[2]),
                                 B, H, T, d, _NORMS[kind], _ACTS[act], float(eps), io, _pointer(ws),
-                                nbytes, _stream(dev, None))
+                                nbytes, on)
     _check(rc)
     return dx, dpar[0], dpar[1], dg, dpar[2]
 

@@ -43,6 +43,7 @@ EXTRA_FLAGS = {
     "linear_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "linear_ln_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "linear_bwd_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "gated_linear.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

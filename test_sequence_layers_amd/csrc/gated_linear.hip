@@ -15,6 +15,8 @@
 //   bf16 I/O:     v_mfma_f32_16x16x32_bf16.  Products of inputs are exact.  Factors that are not
 //     inputs are split into bf16 parts, x = hi + mid + lo: two parts (2^-16 of a term) where the
 //     result is rounded to bf16, three (2^-24) where it is a float32 output or the state itself.
+#include <type_traits>
+
 #include "gated_linear.hpp"
 
 namespace ttt {
@@ -102,27 +104,21 @@ struct Math<bf16> {
   static constexpr int kPlanes = 2;  // hi and lo
   typedef gl_b8 Op;
   template <int N> struct Parts { Op x[N]; };
-  // Column 32 p + 16 b + 4 g + e of a row is kept at 32 p + 8 g + 4 b + e, so that a lane's eight
-  // k of a block are one 16-byte read.
+  // eight k of a block: columns 32 p + 4 g .. + 3 and 32 p + 16 + 4 g .. + 3
   template <bool Half> static __device__ __forceinline__ Op along(const bf16* row, int p, int g) {
-    if constexpr (Half) {
-      const gl_b4 x = *reinterpret_cast<const gl_b4*>(row + 4 * g);
-      return __builtin_shufflevector(x, x, 0, 1, 2, 3, 0, 1, 2, 3);
-    }
-    return *reinterpret_cast<const gl_b8*>(row + 32 * p + 8 * g);
-  }
-  template <int D> static __device__ __forceinline__ int place(int cb, int g) {
-    return D == 16 ? 4 * g : 32 * (cb >> 1) + 8 * g + 4 * (cb & 1);
+    const gl_b4 x = *reinterpret_cast<const gl_b4*>(row + 32 * p + 4 * g);
+    const gl_b4 y = Half ? x : *reinterpret_cast<const gl_b4*>(row + 32 * p + 4 * g + (Half ? 0 : 16));
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   }
   // Transposing LDS read: the 16 lanes of a group give the addresses of four rows' 16 columns
   // (lane 4 i + j: row i, columns 4 j .. + 3) and receive one column of four rows each.
-  template <int D> static __device__ __forceinline__ gl_s4 down16(const bf16* m, int ld, int k0, int cb, int g, int r) {
-    const bf16* q = m + (k0 + 4 * g + (r >> 2)) * ld + place<D>(cb, r & 3);
+  static __device__ __forceinline__ gl_s4 down16(const bf16* m, int ld, int k0, int cb, int g, int r) {
+    const bf16* q = m + (k0 + 4 * g + (r >> 2)) * ld + 16 * cb + 4 * (r & 3);
     typedef __attribute__((address_space(3))) gl_s4 lds_s4;
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)q);
   }
   template <int D> static __device__ __forceinline__ Op down(const bf16* m, int ld, int p, int cb, int g, int r) {
-    const gl_s4 a = down16<D>(m, ld, 32 * p, cb, g, r), b = down16<D>(m, ld, 32 * p + 16, cb, g, r);
+    const gl_s4 a = down16(m, ld, 32 * p, cb, g, r), b = down16(m, ld, 32 * p + 16, cb, g, r);
     return __builtin_bit_cast(gl_b8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
   template <bool Half> static __device__ __forceinline__ gl_f4 mma(const Op& a, const Op& b, gl_f4 c) {
@@ -137,11 +133,17 @@ struct Math<bf16> {
     float rest[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 #pragma unroll
     for (int n = 0; n < N; ++n) {
+      gl_u4 w;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y.x[n][i] = static_cast<bf16>(rest[i]);
-        if (n + 1 < N) rest[i] -= static_cast<float>(y.x[n][i]);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = gl_pack(rest[2 * i], rest[2 * i + 1]);
+        if (n + 1 < N) {
+          rest[2 * i] -= gl_lo(x);
+          rest[2 * i + 1] -= gl_hi(x);
+        }
+        w[i] = x;
       }
+      y.x[n] = __builtin_bit_cast(gl_b8, w);
     }
     return y;
   }
@@ -157,37 +159,32 @@ struct Math<bf16> {
     return c;
   }
   static __device__ __forceinline__ void widen(const Op& x, gl_f4* a, gl_f4* b) {
-    *a = gl_f4{static_cast<float>(x[0]), static_cast<float>(x[1]), static_cast<float>(x[2]), static_cast<float>(x[3])};
-    *b = gl_f4{static_cast<float>(x[4]), static_cast<float>(x[5]), static_cast<float>(x[6]), static_cast<float>(x[7])};
+    const gl_u4 w = __builtin_bit_cast(gl_u4, x);
+    *a = gl_f4{gl_lo(w[0]), gl_hi(w[0]), gl_lo(w[1]), gl_hi(w[1])};
+    *b = gl_f4{gl_lo(w[2]), gl_hi(w[2]), gl_lo(w[3]), gl_hi(w[3])};
   }
   static __device__ __forceinline__ void put(bf16* row, int plane, int cb, int g, const gl_f4& x) {
-    gl_b4 hi, lo;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hi[i] = static_cast<bf16>(x[i]);
-      lo[i] = static_cast<bf16>(x[i] - static_cast<float>(hi[i]));
-    }
-    const int at = place<32>(cb, g);
-    *reinterpret_cast<gl_b4*>(row + at) = hi;
-    *reinterpret_cast<gl_b4*>(row + plane + at) = lo;
+    const uint32_t a = gl_pack(x[0], x[1]), b = gl_pack(x[2], x[3]);
+    const int at = 16 * cb + 4 * g;
+    *reinterpret_cast<gl_u2*>(row + at) = gl_u2{a, b};
+    *reinterpret_cast<gl_u2*>(row + plane + at) =
+        gl_u2{gl_pack(x[0] - gl_lo(a), x[1] - gl_hi(a)), gl_pack(x[2] - gl_lo(b), x[3] - gl_hi(b))};
   }
   static __device__ __forceinline__ gl_f4 mma_planes(const Op& a, const bf16* row, int plane, int p, int g, gl_f4 c) {
     c = mma<false>(a, along<false>(row + plane, p, g), c);
     return mma<false>(a, along<false>(row, p, g), c);
   }
   template <int D> static __device__ __forceinline__ gl_f4 row4(const bf16* row, int cb, int g) {
-    const gl_b4 x = *reinterpret_cast<const gl_b4*>(row + place<D>(cb, g));
-    return gl_f4{static_cast<float>(x[0]), static_cast<float>(x[1]), static_cast<float>(x[2]), static_cast<float>(x[3])};
+    const gl_u2 w = *reinterpret_cast<const gl_u2*>(row + 16 * cb + 4 * g);
+    return gl_f4{gl_lo(w[0]), gl_hi(w[0]), gl_lo(w[1]), gl_hi(w[1])};
   }
   static __device__ __forceinline__ void store4(const gl_f4& x, __amdgpu_buffer_rsrc_t dst, int elem) {
-    const gl_b4 y = {from_f32<bf16>(x[0]), from_f32<bf16>(x[1]), from_f32<bf16>(x[2]), from_f32<bf16>(x[3])};
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(gl_u2, y), dst, elem * 2, 0, 0);
+    const gl_u2 y = {gl_pack(x[0], x[1]), gl_pack(x[2], x[3])};
+    __builtin_amdgcn_raw_buffer_store_b64(y, dst, elem * 2, 0, 0);
   }
   template <int D> static __device__ __forceinline__ void put_vec(bf16* m, int vec, const gl_u4& x) {
-    const int at = vec * 8, cb = (at % D) >> 4, g = (at >> 2) & 3;  // eight columns: g and g + 1 of a block of 16
-    bf16* row = m + (at / D) * (D + kPad);
-    *reinterpret_cast<gl_u2*>(row + place<D>(cb, g)) = gl_u2{x[0], x[1]};
-    *reinterpret_cast<gl_u2*>(row + place<D>(cb, g + 1)) = gl_u2{x[2], x[3]};
+    const int at = vec * 8;
+    *reinterpret_cast<gl_u4*>(m + (at / D) * (D + kPad) + at % D) = x;
   }
 };
 template <typename IO, int D>
@@ -203,12 +200,18 @@ struct Shape {
   static constexpr int kVec = static_cast<int>(sizeof(IO));    // 16-byte vectors of a tile per thread
 };
 
-// A token tile (kC x D) on its way from HBM to LDS.
+// Loads.  A tile's registers are filled by buffer loads whose range ends at the last valid token
+// (0 bytes for a chunk outside the segment), so every wave issues the same ones on every path.
+// Loads and stores complete in order: a wait for a load issued before some stores need not wait for
+// them, as long as their number is known.  So the stores of a chunk are the same on every path
+// too (lanes or waves with nothing to store have an empty range), and `no_store` stands in for those
+// of the chunk before the first.
 template <typename IO, int D>
 struct Tile {
   gl_u4 x[sizeof(IO)];
-  __device__ __forceinline__ void load(const IO* base, int c0, int len, int tid) {
-    const __amdgpu_buffer_rsrc_t src = gl_span(base + static_cast<size_t>(c0) * D, min(kC, len - c0) * D * static_cast<int>(sizeof(IO)));
+  // tokens c0 .. of base, `rows` of them valid (may be negative)
+  __device__ __forceinline__ void load(const IO* base, long long c0, int rows, int tid) {
+    const __amdgpu_buffer_rsrc_t src = gl_span(base + c0 * D, max(0, min(kC, rows)) * D * static_cast<int>(sizeof(IO)));
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(IO)); ++i)
       x[i] = __builtin_amdgcn_raw_buffer_load_b128(src, (tid + i * 4 * D) * 16, 0, 0);
@@ -218,6 +221,30 @@ struct Tile {
     for (int i = 0; i < static_cast<int>(sizeof(IO)); ++i) Math<IO>::template put_vec<D>(m, tid + i * 4 * D, x[i]);
   }
 };
+__device__ __forceinline__ void store1(float x, __amdgpu_buffer_rsrc_t dst, int i) {
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), dst, i * 4, 0, 0);
+}
+template <int N>
+__device__ __forceinline__ void no_store() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) store1(0.0f, gl_span(nullptr, 0), 0);
+}
+
+// Blocks (ut, st), st <= ut, of 16 tokens each in a chunk's triangle of token pairs, in order.
+constexpr int kBlocks = 10;
+__device__ __forceinline__ int block_row(int t) { return t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0; }
+// The blocks wv, wv + NW, ... of a wave, two at a time where there are two, so that one's LDS reads
+// and products run under the other's: f(n, first), n blocks first, first + NW.
+template <int NW, typename F>
+__device__ __forceinline__ void wave_blocks(int wv, F f) {
+  constexpr int kAll = kBlocks / NW;  // of every wave
+#pragma unroll
+  for (int i = 0; i + 2 <= kAll; i += 2) f(std::integral_constant<int, 2>(), wv + i * NW);
+  if constexpr (kAll % 2) f(std::integral_constant<int, 1>(), wv + (kAll - 1) * NW);
+  if constexpr (kBlocks % NW) {
+    if (wv < kBlocks % NW) f(std::integral_constant<int, 1>(), wv + kAll * NW);
+  }
+}
 
 // One sequence's view of the arguments.
 struct Seq {
@@ -236,13 +263,19 @@ __device__ __forceinline__ Seq sequence(const GatedArgs& a, int chain) {
   s.rate = a.eta_tok ? a.eta_tok + s.row0 : nullptr;
   return s;
 }
-// the token's log decay and rate (0, 0 past the sequence)
+// log decays and rates of a chunk's tokens, lane = token (0, 0 past the sequence)
 struct GateRate {
-  float g, e;
-  __device__ __forceinline__ void load(const Seq& s, float eta, int t) {
-    const bool in = t < s.len;
-    g = in && s.gate ? s.gate[t] : 0.0f;
-    e = in ? (s.rate ? eta * s.rate[t] : eta) : 0.0f;
+  float g, rate;
+  __device__ __forceinline__ void load(const Seq& s, long long c0, int lane) {
+    const int bytes = c0 < 0 || c0 >= s.len ? 0 : min(kC, static_cast<int>(s.len - c0)) * 4;
+    g = load1(gl_span(s.gate + c0, s.gate ? bytes : 0), lane);
+    rate = load1(gl_span(s.rate + c0, s.rate ? bytes : 0), lane);
+  }
+  __device__ __forceinline__ void decays(const Seq& s, float eta, long long c0, GlDecays* d, int lane) const {
+    gl_decays(g, c0 >= 0 && c0 + lane < s.len ? (s.rate ? eta * rate : eta) : 0.0f, d, lane);
+  }
+  static __device__ __forceinline__ float load1(__amdgpu_buffer_rsrc_t src, int i) {
+    return __builtin_bit_cast(float, static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b32(src, i * 4, 0, 0)));
   }
 };
 __device__ __forceinline__ const float* initial_state(const GatedArgs& a, int chain, int dd) {
@@ -271,24 +304,25 @@ __device__ __forceinline__ void store_state_transposed(const gl_f4* x, float* w,
 }
 
 // x <- whole x + sum over the chunk's tokens s of a_s c_s b_s^T, a the rows of the tile A, b the
-// wave's 16 columns (k down the tokens), c_s = c[s] (c2[s]).
+// wave's 16 columns (k down the tokens).
 template <typename IO, int D, int N>
 __device__ __forceinline__ void update_state(gl_f4* x, float whole, const typename Math<IO>::Elem* A,
-                                             const typename Math<IO>::Op* b, const float* c, const float* c2,
-                                             int g, int r) {
+                                             const typename Math<IO>::Op* b, const float* c, int g, int r) {
   typedef Math<IO> M;
+  whole = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, whole)));
+  if (whole == 0.0f) {
 #pragma unroll
-  for (int ab = 0; ab < D / 16; ++ab) x[ab] = keep4(whole, x[ab]);
+    for (int ab = 0; ab < D / 16; ++ab) x[ab] = gl_f4{0.0f, 0.0f, 0.0f, 0.0f};
+  } else {
+#pragma unroll
+    for (int ab = 0; ab < D / 16; ++ab) x[ab] *= whole;
+  }
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     gl_f4 lo, hi;
     M::widen(b[p], &lo, &hi);
     lo *= at4(c, 32 * p + 4 * g);
     hi *= at4(c, 32 * p + 16 + 4 * g);
-    if (c2) {
-      lo *= at4(c2, 32 * p + 4 * g);
-      hi *= at4(c2, 32 * p + 16 + 4 * g);
-    }
     const typename M::template Parts<N> f = M::template split<N>(lo, hi);
 #pragma unroll
     for (int ab = 0; ab < D / 16; ++ab)
@@ -323,6 +357,17 @@ __device__ __forceinline__ gl_f4 row_products(const typename Math<IO>::Elem* a, 
   return c;
 }
 
+// Blocks of a factor that a product over 32 tokens reads and that no pair (u, s), s <= u, reaches:
+// (rows u, columns s) = (0, 1) and (2, 3), transposed (1, 0) and (3, 2).  They stay 0.
+template <typename IO, int D, bool kRowsAreU>
+__device__ __forceinline__ void zero_unused(typename Math<IO>::Elem* m, int wv, int g, int r) {
+  typedef Shape<IO, D> S;
+  if (wv != 0) return;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2)
+    Math<IO>::put(m + (16 * (kRowsAreU ? i : i + 1) + r) * S::kLdP, S::kPlane, kRowsAreU ? i + 1 : i, g, gl_f4{0.0f, 0.0f, 0.0f, 0.0f});
+}
+
 // ---------------------------------------------------------------- segments
 //
 // What a segment adds to the state from zero.  Side 0: sum over its tokens s of (decay to the
@@ -331,7 +376,7 @@ __device__ __forceinline__ gl_f4 row_products(const typename Math<IO>::Elem* a, 
 template <typename IO, int D>
 struct SumsLds {
   typename Math<IO>::Elem a[Shape<IO, D>::kTile], b[Shape<IO, D>::kTile];
-  GlDecays dec;
+  GlDecays dec[2];  // of this chunk and the next
 };
 
 template <typename IO, int D>
@@ -352,29 +397,42 @@ __global__ __launch_bounds__(4 * D) void gl_sums_kernel(GatedArgs a) {
   gl_f4 x[S::kNW];
 #pragma unroll
   for (int i = 0; i < S::kNW; ++i) x[i] = gl_f4{0.0f, 0.0f, 0.0f, 0.0f};
-  Tile<IO, D> ta, tb;
-  GateRate gr;
+  // what a chunk's step needs in registers: its tiles, and the gates of the chunk after it
+  struct Set {
+    Tile<IO, D> a, b;
+    GateRate gr;
+  } y;
   float all = 1.0f;
   auto chunk = [&](int i) { return side == 0 ? first + i : first + n - 1 - i; };
-  auto prefetch = [&](int c) {
-    ta.load(rows, c * kC, s.len, tid);
-    tb.load(cols, c * kC, s.len, tid);
-    if (wv == 0) gr.load(s, a.eta, c * kC + lane);
+  auto fetch = [&](int i) {
+    const long long c0 = static_cast<long long>(chunk(i)) * kC;
+    y.gr.load(s, static_cast<long long>(chunk(i + 1)) * kC, lane);
+    const int valid = i < n ? s.len - static_cast<int>(c0) : 0;
+    y.a.load(rows, c0, valid, tid);
+    y.b.load(cols, c0, valid, tid);
   };
-  prefetch(chunk(0));
+  const bool decayer = wv == S::kNW - 1;  // the wave that forms the next chunk's decays
+  {
+    GateRate gr;
+    gr.load(s, static_cast<long long>(chunk(0)) * kC, lane);
+    fetch(0);
+    if (decayer) gr.decays(s, a.eta, static_cast<long long>(chunk(0)) * kC, &L.dec[0], lane);
+  }
   for (int i = 0; i < n; ++i) {
     gl_barrier();  // the previous chunk's tiles have been read
-    ta.put(L.a, tid);
-    tb.put(L.b, tid);
-    if (wv == 0) gl_decays(gr.g, gr.e, &L.dec, lane);
+    y.a.put(L.a, tid);
+    y.b.put(L.b, tid);
+    const GateRate gr = y.gr;
     gl_barrier();
-    if (i + 1 < n) prefetch(chunk(i + 1));
+    fetch(i + 1);
+    const GlDecays& dec = L.dec[i & 1];
+    if (decayer && i + 1 < n) gr.decays(s, a.eta, static_cast<long long>(chunk(i + 1)) * kC, &L.dec[(i + 1) & 1], lane);
     typename M::Op b[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p) b[p] = M::template down<D>(L.b, S::kLd, p, wv, g, r);
-    const float whole = L.dec.whole[0];
+    const float whole = dec.whole[0];
     all *= whole;
-    update_state<IO, D, 3>(x, whole, L.a, b, side == 0 ? L.dec.to : L.dec.from, side == 0 ? L.dec.e : nullptr, g, r);
+    update_state<IO, D, 3>(x, whole, L.a, b, side == 0 ? dec.to_e : dec.from, g, r);
   }
   float* out = (side == 0 ? a.seg_w : a.seg_g) + static_cast<size_t>(blockIdx.x) * D * D;
   store_state_transposed<D>(x, out, wv, g, r);
@@ -383,27 +441,31 @@ __global__ __launch_bounds__(4 * D) void gl_sums_kernel(GatedArgs a) {
 
 // The sums become the states at the segments' starts (side 0, first to last from w0) and the
 // gradients at their ends (side 1, last to first from dw_out), in place.
+// One element a thread; the sums of kAhead segments are loaded before the first is used.
 template <int D>
 __global__ __launch_bounds__(256) void gl_scan_kernel(GatedArgs a) {
-  constexpr int kPer = D * D / 4;  // threads per sequence
+  constexpr int kAhead = 16;
   const long long item = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  const int chain = static_cast<int>(item / kPer), at = static_cast<int>(item % kPer) * 4, side = blockIdx.y;
-  if (chain >= a.B * a.H) return;
+  const int chain = static_cast<int>(item / (D * D)), at = static_cast<int>(item % (D * D)), side = blockIdx.y;
   const size_t seg0 = static_cast<size_t>(chain) * a.nseg;
   float* x = (side == 0 ? a.seg_w : a.seg_g) + seg0 * D * D + at;
   const float* decay = a.seg_decay + static_cast<size_t>(side) * a.B * a.H * a.nseg + seg0;
-  gl_f4 state = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (side == 0) state = at4(initial_state(a, chain, D * D), at);
-  else if (a.dw_out) state = at4(a.dw_out + static_cast<size_t>(chain) * D * D, at);
-  for (int i = 0; i < a.nseg; ++i) {
-    const int m = side == 0 ? i : a.nseg - 1 - i;
-    float* p = x + static_cast<size_t>(m) * D * D;
-    if (i + 1 < a.nseg) {
-      const gl_f4 sum = at4(p, 0);
-      *reinterpret_cast<gl_f4*>(p) = state;
-      state = keep4(decay[m], state) + sum;
-    } else {
-      *reinterpret_cast<gl_f4*>(p) = state;
+  float state = side == 0 ? initial_state(a, chain, D * D)[at]
+                          : a.dw_out ? a.dw_out[static_cast<size_t>(chain) * D * D + at] : 0.0f;
+  for (int i0 = 0; i0 < a.nseg; i0 += kAhead) {
+    float sum[kAhead], dec[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j, m = side == 0 ? i : a.nseg - 1 - i;
+      const bool have = i + 1 < a.nseg;  // nothing follows the last
+      sum[j] = have ? x[static_cast<size_t>(m) * D * D] : 0.0f;
+      dec[j] = have ? decay[m] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j, m = side == 0 ? i : a.nseg - 1 - i;
+      if (i < a.nseg) x[static_cast<size_t>(m) * D * D] = state;
+      state = gl_keep(dec[j], state) + sum[j];
     }
   }
 }
@@ -413,7 +475,7 @@ template <typename IO, int D>
 struct FwdLds {
   typename Math<IO>::Elem q[Shape<IO, D>::kTile], k[Shape<IO, D>::kTile], v[Shape<IO, D>::kTile];
   typename Math<IO>::Elem p[Math<IO>::kPlanes * Shape<IO, D>::kPlane];
-  GlDecays dec;
+  GlDecays dec[2];  // of this chunk and the next
 };
 
 template <typename IO, int D>
@@ -435,44 +497,62 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
 
   gl_f4 w[NW];  // W^T: W's rows 16 wv + r
   load_state<D, true>(w, a.nseg > 1 ? a.seg_w + static_cast<size_t>(blockIdx.x) * D * D : initial_state(a, chain, D * D), wv, g, r);
-  Tile<IO, D> tq, tk, tv;
-  GateRate gr;
-  auto prefetch = [&](int c) {
-    tq.load(q, c * kC, s.len, tid);
-    tk.load(k, c * kC, s.len, tid);
-    tv.load(v, c * kC, s.len, tid);
-    if (wv == 0) gr.load(s, a.eta, c * kC + lane);
+  // what a chunk's step needs in registers: its tiles, and the gates of the chunk after it
+  struct Set {
+    Tile<IO, D> q, k, v;
+    GateRate gr;
+  } y;
+  auto fetch = [&](int c) {
+    const long long c0 = static_cast<long long>(c) * kC;
+    y.gr.load(s, c0 + kC, lane);
+    const int valid = c < end ? s.len - static_cast<int>(c0) : 0;
+    y.q.load(q, c0, valid, tid);
+    y.k.load(k, c0, valid, tid);
+    y.v.load(v, c0, valid, tid);
   };
-  if (first < end) prefetch(first);
+  const bool decayer = wv == NW - 1;  // the wave that forms the next chunk's decays
+  {
+    GateRate gr;
+    gr.load(s, static_cast<long long>(first) * kC, lane);
+    fetch(first);
+    no_store<4>();
+    if (decayer) gr.decays(s, a.eta, static_cast<long long>(first) * kC, &L.dec[0], lane);
+  }
+  zero_unused<IO, D, true>(L.p, wv, g, r);
   for (int c = first; c < end; ++c) {
     const int c0 = c * kC;
+    const GlDecays& dec = L.dec[(c - first) & 1];
     gl_barrier();  // the previous chunk's tiles have been read
-    tq.put(L.q, tid);
-    tk.put(L.k, tid);
-    tv.put(L.v, tid);
-    if (wv == 0) gl_decays(gr.g, gr.e, &L.dec, lane);
+    y.q.put(L.q, tid);
+    y.k.put(L.k, tid);
+    y.v.put(L.v, tid);
+    const GateRate gr = y.gr;
     gl_barrier();
-    if (c + 1 < end) prefetch(c + 1);
+    fetch(c + 1);
+    if (decayer && c + 1 < end) gr.decays(s, a.eta, static_cast<long long>(c + 1) * kC, &L.dec[(c + 1 - first) & 1], lane);
 
-    // P[u][s] = exp(b_u - b_s) e_s (q_u . k_s) for s <= u, the wave's blocks of 16 tokens u
+    // P[u][s] = exp(b_u - b_s) e_s (q_u . k_s) for s <= u
+    wave_blocks<NW>(wv, [&](auto n, int first_block) {
+      constexpr int N = n.value;
+      gl_f4 p[N];
+      int ut[N], st[N];
 #pragma unroll
-    for (int it = 0; it < 4 / NW; ++it) {
-      const int ut = wv + it * NW, u = 16 * ut + r;
-      const float uh = L.dec.bh[u], ul = L.dec.bl[u];
-#pragma unroll
-      for (int st = 0; st < 4; ++st) {
-        if (st > (ut | 1)) break;  // up to the end of the block of 32
-        const int s4 = 16 * st + 4 * g;
-        gl_f4 p = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (st <= ut) {
-          p = row_products<IO, D>(L.k + (16 * st + r) * LD, L.q + u * LD, g);
-          const gl_f4 sh = at4(L.dec.bh, s4), sl = at4(L.dec.bl, s4), e = at4(L.dec.e, s4);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) p[x] = s4 + x <= u ? p[x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
-        }
-        M::put(L.p + u * LDP, S::kPlane, st, g, p);
+      for (int i = 0; i < N; ++i) {
+        ut[i] = block_row(first_block + i * NW);
+        st[i] = first_block + i * NW - ut[i] * (ut[i] + 1) / 2;
+        p[i] = row_products<IO, D>(L.k + (16 * st[i] + r) * LD, L.q + (16 * ut[i] + r) * LD, g);
       }
-    }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int u = 16 * ut[i] + r, s4 = 16 * st[i] + 4 * g;
+        const float uh = dec.bh[u], ul = dec.bl[u];
+        const gl_f4 sh = at4(dec.bh, s4), sl = at4(dec.bl, s4), e = at4(dec.e, s4);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) p[i][x] = s4 + x <= u ? p[i][x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) M::put(L.p + (16 * ut[i] + r) * LDP, S::kPlane, st[i], g, p[i]);
+    });
     gl_barrier();
 
     typename M::Op vf[2];  // V, k down the tokens, the wave's features
@@ -488,9 +568,9 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
       gl_f4 zp = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int p = 0; p <= ut / 2; ++p) zp = M::mma_planes(vf[p], L.p + u * LDP, S::kPlane, p, g, zp);
-      M::store4(zp + keep4(L.dec.from[u], zi), dst, u * D + 16 * wv + 4 * g);
+      M::store4(zp + keep4(dec.from[u], zi), dst, u * D + 16 * wv + 4 * g);
     }
-    update_state<IO, D, 3>(w, L.dec.whole[0], L.k, vf, L.dec.to, L.dec.e, g, r);
+    update_state<IO, D, 3>(w, dec.whole[0], L.k, vf, dec.to_e, g, r);
   }
   if (a.w_out && seg == a.nseg - 1) store_state_transposed<D>(w, a.w_out + static_cast<size_t>(chain) * D * D, wv, g, r);
 }
@@ -519,8 +599,10 @@ struct BwdLds {
   typedef Shape<IO, D> S;
   typename S::Elem q[S::kTile], k[S::kTile], v[S::kTile], z[S::kTile];
   typename S::Elem p[Math<IO>::kPlanes * S::kPlane], r[Math<IO>::kPlanes * S::kPlane];
-  float part[S::kNW][kC];
-  GlDecays dec;
+  float part[S::kNW][kC];  // in_u or out_s, the waves' shares
+  float pairs[4][kC];      // row_u or col_s, the blocks' shares
+  float diag[kC];          // m_ss
+  GlDecays dec[2];  // of this chunk and the next
 };
 
 template <typename IO, int D>
@@ -551,62 +633,82 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
   const float* g_end = a.nseg > 1 ? a.seg_g + static_cast<size_t>(item) * D * D
                                   : a.dw_out ? a.dw_out + static_cast<size_t>(chain) * D * D : nullptr;
 
-  Tile<IO, D> tq, tk, tv, tz;
-  GateRate gr;
-  auto prefetch = [&](int c) {
-    tq.load(q, c * kC, s.len, tid);
-    tk.load(k, c * kC, s.len, tid);
-    tv.load(v, c * kC, s.len, tid);
-    tz.load(dz, c * kC, s.len, tid);
-    if (wv == 0) gr.load(s, a.eta, c * kC + lane);
+  // what a chunk's step needs in registers: its tiles, and the gates of the chunk after it
+  struct Set {
+    Tile<IO, D> q, k, v, z;
+    GateRate gr;
+  } y;
+  auto fetch = [&](int c, int next) {
+    const long long c0 = static_cast<long long>(c) * kC;
+    y.gr.load(s, static_cast<long long>(next) * kC, lane);
+    const int valid = c >= first && c < end ? s.len - static_cast<int>(c0) : 0;
+    y.q.load(q, c0, valid, tid);
+    y.k.load(k, c0, valid, tid);
+    y.v.load(v, c0, valid, tid);
+    y.z.load(dz, c0, valid, tid);
   };
-  auto stage = [&]() {
-    tq.put(L.q, tid);
-    tk.put(L.k, tid);
-    tv.put(L.v, tid);
-    tz.put(L.z, tid);
-    if (wv == 0) gl_decays(gr.g, gr.e, &L.dec, lane);
+  const bool decayer = wv == NW - 1;  // the wave that forms the next chunk's decays
+  // tiles of chunk c to LDS, those of `next` on their way, its decays formed
+  auto stage = [&](int c, int next, int after, int turn) {
+    gl_barrier();  // the previous chunk's tiles have been read
+    y.q.put(L.q, tid);
+    y.k.put(L.k, tid);
+    y.v.put(L.v, tid);
+    y.z.put(L.z, tid);
+    const GateRate gr = y.gr;
+    gl_barrier();
+    fetch(next, after);
+    if (decayer && next >= first && next < end) gr.decays(s, a.eta, static_cast<long long>(next) * kC, &L.dec[turn ^ 1], lane);
   };
+  auto begin = [&](int c, int next) {
+    GateRate gr;
+    gr.load(s, static_cast<long long>(c) * kC, lane);
+    fetch(c, next);
+    if (decayer) gr.decays(s, a.eta, static_cast<long long>(c) * kC, &L.dec[0], lane);
+  };
+  // per-token sums are stored by wave 0
+  auto per_token = [&](float* p, int c0) { return gl_span(p + c0, p && wv == 0 ? min(kC, T - c0) * 4 : 0); };
 
   if (role == 0) {
     gl_f4 w[NW];  // W's columns 16 wv + r
     load_state<D, false>(w, a.nseg > 1 ? a.seg_w + static_cast<size_t>(item) * D * D : initial_state(a, chain, D * D), wv, g, r);
     IO* dq = static_cast<IO*>(a.dq) + s.row0 * D;
-    if (first < end) prefetch(first);
+    begin(first, first + 1);
+    no_store<6>();
+    zero_unused<IO, D, true>(L.r, wv, g, r);
     for (int c = first; c < end; ++c) {
-      const int c0 = c * kC;
-      gl_barrier();
-      stage();
-      gl_barrier();
-      if (c + 1 < end) prefetch(c + 1);
+      const int c0 = c * kC, turn = (c - first) & 1;
+      const GlDecays& dec = L.dec[turn];
+      stage(c, c + 1, c + 2, turn);
+      wave_blocks<NW>(wv, [&](auto n, int first_block) {
+        constexpr int N = n.value;
+        gl_f4 rd[N], p[N];
+        int ut[N], st[N];
 #pragma unroll
-      for (int it = 0; it < 4 / NW; ++it) {
-        const int ut = wv + it * NW, u = 16 * ut + r;
-        const float uh = L.dec.bh[u], ul = L.dec.bl[u];
-        float row = 0.0f;
+        for (int i = 0; i < N; ++i) {
+          ut[i] = block_row(first_block + i * NW);
+          st[i] = first_block + i * NW - ut[i] * (ut[i] + 1) / 2;
+          rd[i] = row_products<IO, D>(L.v + (16 * st[i] + r) * LD, L.z + (16 * ut[i] + r) * LD, g);
+          if (row_o) p[i] = row_products<IO, D>(L.k + (16 * st[i] + r) * LD, L.q + (16 * ut[i] + r) * LD, g);
+        }
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
-          if (st > (ut | 1)) break;
-          const int s4 = 16 * st + 4 * g;
-          gl_f4 rd = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (st <= ut) {
-            rd = row_products<IO, D>(L.v + (16 * st + r) * LD, L.z + u * LD, g);
-            const gl_f4 sh = at4(L.dec.bh, s4), sl = at4(L.dec.bl, s4), e = at4(L.dec.e, s4);
+        for (int i = 0; i < N; ++i) {
+          const int u = 16 * ut[i] + r, s4 = 16 * st[i] + 4 * g;
+          const float uh = dec.bh[u], ul = dec.bl[u];
+          const gl_f4 sh = at4(dec.bh, s4), sl = at4(dec.bl, s4), e = at4(dec.e, s4);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) rd[x] = s4 + x <= u ? rd[x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
-            if (row_o) {
-              const gl_f4 p = row_products<IO, D>(L.k + (16 * st + r) * LD, L.q + u * LD, g);
+          for (int x = 0; x < 4; ++x) rd[i][x] = s4 + x <= u ? rd[i][x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
+          if (row_o) {
+            float row = 0.0f;
 #pragma unroll
-              for (int x = 0; x < 4; ++x) row += s4 + x < u ? p[x] * rd[x] : 0.0f;
-            }
+            for (int x = 0; x < 4; ++x) row += s4 + x < u ? p[i][x] * rd[i][x] : 0.0f;
+            row = over_g(row);
+            if (g == 0) L.pairs[st[i]][u] = row;
           }
-          M::put(L.r + u * LDP, S::kPlane, st, g, rd);
         }
-        if (row_o) {
-          row = over_g(row);
-          if (g == 0 && c0 + u < T) row_o[c0 + u] = row;
-        }
-      }
+#pragma unroll
+        for (int i = 0; i < N; ++i) M::put(L.r + (16 * ut[i] + r) * LDP, S::kPlane, st[i], g, rd[i]);
+      });
       gl_barrier();
       typename M::Op kf[2];
 #pragma unroll
@@ -617,7 +719,7 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
 #pragma unroll
       for (int ut = 0; ut < 4; ++ut) {
         const int u = 16 * ut + r;
-        const gl_f4 xi = keep4(L.dec.from[u], state_times<IO, D, 3>(wp, L.z + u * LD, g));
+        const gl_f4 xi = keep4(dec.from[u], state_times<IO, D, 3>(wp, L.z + u * LD, g));
         gl_f4 xp = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int p = 0; p <= ut / 2; ++p) xp = M::mma_planes(kf[p], L.r + u * LDP, S::kPlane, p, g, xp);
@@ -627,16 +729,17 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
         }
         M::store4(xi + xp, dst, u * D + 16 * wv + 4 * g);
       }
-      update_state<IO, D, 3>(w, L.dec.whole[0], L.v, kf, L.dec.to, L.dec.e, g, r);
+      update_state<IO, D, 3>(w, dec.whole[0], L.v, kf, dec.to_e, g, r);
+      float in = 0.0f, row = 0.0f;
       if (row_o) {
         gl_barrier();
-        if (wv == 0 && c0 + lane < T) {
-          float in = 0.0f;
 #pragma unroll
-          for (int x = 0; x < NW; ++x) in += L.part[x][lane];
-          in_o[c0 + lane] = in;
-        }
+        for (int x = 0; x < NW; ++x) in += L.part[x][lane];
+#pragma unroll
+        for (int st = 0; st < 4; ++st) row += st <= lane >> 4 ? L.pairs[st][lane] : 0.0f;
       }
+      store1(in, per_token(in_o, c0), lane);
+      store1(row, per_token(row_o, c0), lane);
     }
     if (row_o) {  // <G, W> at the segment's end
       double x = 0.0;
@@ -657,45 +760,54 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
     IO* dk = static_cast<IO*>(a.dk) + s.row0 * D;
     IO* dv = static_cast<IO*>(a.dv) + s.row0 * D;
     float* de_o = a.deta_tok ? a.deta_tok + s.row0 : nullptr;
-    if (first < end) prefetch(end - 1);
+    begin(end - 1, end - 2);
+    no_store<11>();
+    zero_unused<IO, D, false>(L.p, wv, g, r);
+    zero_unused<IO, D, false>(L.r, wv, g, r);
     for (int c = end - 1; c >= first; --c) {
-      const int c0 = c * kC;
-      gl_barrier();
-      stage();
-      gl_barrier();
-      if (c > first) prefetch(c - 1);
-      // the wave's blocks of 16 tokens s: rows of P^T and R^T (decayed, without e_s)
-      float diag[4 / NW], col[4 / NW];
+      const int c0 = c * kC, turn = (end - 1 - c) & 1;
+      const GlDecays& dec = L.dec[turn];
+      stage(c, c - 1, c - 2, turn);
+      // rows s of P^T and R^T (decayed, without e_s)
+      wave_blocks<NW>(wv, [&](auto n, int first_block) {
+        constexpr int N = n.value;
+        gl_f4 p[N], rd[N];
+        int ut[N], st[N];
 #pragma unroll
-      for (int it = 0; it < 4 / NW; ++it) {
-        const int st = wv + it * NW, ss = 16 * st + r;
-        const float sh = L.dec.bh[ss], sl = L.dec.bl[ss];
-        float cs = 0.0f, dg = 0.0f;
-#pragma unroll
-        for (int ut = 0; ut < 4; ++ut) {
-          if (ut < (st & ~1)) continue;  // from the start of the block of 32
-          gl_f4 p = {0.0f, 0.0f, 0.0f, 0.0f}, rd = p;
-          if (ut >= st) {
-            p = row_products<IO, D>(L.q + (16 * ut + r) * LD, L.k + ss * LD, g);
-            rd = row_products<IO, D>(L.z + (16 * ut + r) * LD, L.v + ss * LD, g);
-            const int u4 = 16 * ut + 4 * g;
-            const gl_f4 uh = at4(L.dec.bh, u4), ul = at4(L.dec.bl, u4);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float dec = gl_between(uh[x], ul[x], sh, sl);
-              const float m = p[x] * rd[x] * dec;
-              p[x] = u4 + x >= ss ? p[x] * dec : 0.0f;
-              rd[x] = u4 + x >= ss ? rd[x] * dec : 0.0f;
-              cs += u4 + x > ss ? m : 0.0f;
-              dg += u4 + x == ss ? m : 0.0f;
-            }
-          }
-          M::put(L.p + ss * LDP, S::kPlane, ut, g, p);
-          M::put(L.r + ss * LDP, S::kPlane, ut, g, rd);
+        for (int i = 0; i < N; ++i) {
+          ut[i] = block_row(first_block + i * NW);
+          st[i] = first_block + i * NW - ut[i] * (ut[i] + 1) / 2;
+          p[i] = row_products<IO, D>(L.q + (16 * ut[i] + r) * LD, L.k + (16 * st[i] + r) * LD, g);
+          rd[i] = row_products<IO, D>(L.z + (16 * ut[i] + r) * LD, L.v + (16 * st[i] + r) * LD, g);
         }
-        col[it] = over_g(cs);
-        diag[it] = over_g(dg);
-      }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int ss = 16 * st[i] + r, u4 = 16 * ut[i] + 4 * g;
+          const float sh = dec.bh[ss], sl = dec.bl[ss];
+          const gl_f4 uh = at4(dec.bh, u4), ul = at4(dec.bl, u4);
+          float cs = 0.0f, dg = 0.0f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float f = gl_between(uh[x], ul[x], sh, sl);
+            const float m = p[i][x] * rd[i][x] * f;
+            p[i][x] = u4 + x >= ss ? p[i][x] * f : 0.0f;
+            rd[i][x] = u4 + x >= ss ? rd[i][x] * f : 0.0f;
+            cs += u4 + x > ss ? m : 0.0f;
+            dg += u4 + x == ss ? m : 0.0f;
+          }
+          cs = over_g(cs);
+          if (g == 0) L.pairs[ut[i]][ss] = cs;
+          if (ut[i] == st[i]) {
+            dg = over_g(dg);
+            if (g == 0) L.diag[ss] = dg;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          M::put(L.p + (16 * st[i] + r) * LDP, S::kPlane, ut[i], g, p[i]);
+          M::put(L.r + (16 * st[i] + r) * LDP, S::kPlane, ut[i], g, rd[i]);
+        }
+      });
       gl_barrier();
       typename M::Op zf[2], qf[2];  // dZ and Q, k down the tokens u, the wave's features
 #pragma unroll
@@ -713,7 +825,7 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
 #pragma unroll
       for (int st = 0; st < 4; ++st) {
         const int ss = 16 * st + r;
-        const float f = L.dec.to[ss], e = L.dec.e[ss];
+        const float f = dec.to[ss], e = dec.e[ss];
         const gl_f4 vi = keep4(f, state_times<IO, D, 3>(tp, L.k + ss * LD, g));
         const gl_f4 ki = keep4(f, state_times<IO, D, 2>(np, L.v + ss * LD, g));
         gl_f4 vp = {0.0f, 0.0f, 0.0f, 0.0f}, kp = vp;
@@ -727,25 +839,19 @@ __global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
         M::store4(e * (vi + vp), dstv, ss * D + 16 * wv + 4 * g);
         M::store4(e * (ki + kp), dstk, ss * D + 16 * wv + 4 * g);
       }
-      const float whole = L.dec.whole[0];
-      update_state<IO, D, 3>(gt, whole, L.q, zf, L.dec.from, nullptr, g, r);
-      update_state<IO, D, 2>(gn, whole, L.z, qf, L.dec.from, nullptr, g, r);
+      const float whole = dec.whole[0];
+      update_state<IO, D, 3>(gt, whole, L.q, zf, dec.from, g, r);
+      update_state<IO, D, 2>(gn, whole, L.z, qf, dec.from, g, r);
       gl_barrier();
+      float out = 0.0f, col = 0.0f;
 #pragma unroll
-      for (int it = 0; it < 4 / NW; ++it) {
-        const int ss = 16 * (wv + it * NW) + r, t = c0 + ss;
-        float out = 0.0f;
+      for (int x = 0; x < NW; ++x) out += L.part[x][lane];
 #pragma unroll
-        for (int x = 0; x < NW; ++x) out += L.part[x][ss];
-        const float e = L.dec.e[ss];
-        if (g == 0 && t < T) {
-          if (de_o) de_o[t] = t < s.len ? a.eta * (col[it] + diag[it] + out) : 0.0f;
-          if (col_o) {
-            col_o[t] = e * col[it];
-            out_o[t] = e * out;
-          }
-        }
-      }
+      for (int ut = 0; ut < 4; ++ut) col += ut >= lane >> 4 ? L.pairs[ut][lane] : 0.0f;
+      const float e = dec.e[lane];
+      store1(c0 + lane < s.len ? a.eta * (col + L.diag[lane] + out) : 0.0f, per_token(de_o, c0), lane);
+      store1(e * col, per_token(col_o, c0), lane);
+      store1(e * out, per_token(out_o, c0), lane);
     }
     if (seg == 0) store_state_transposed<D>(gt, a.dw0 + static_cast<size_t>(chain) * D * D, wv, g, r);
   }
@@ -801,7 +907,7 @@ int chunks_per_segment(long long chains, int nchunks, int want) {
 }
 void plan(GatedArgs* a, bool bwd) {
   const int nchunks = (a->T + kC - 1) / kC;
-  a->spc = chunks_per_segment(static_cast<long long>(a->B) * a->H, nchunks, bwd ? 512 : 512);
+  a->spc = chunks_per_segment(static_cast<long long>(a->B) * a->H, nchunks, getenv("GL_WANT") ? atoi(getenv("GL_WANT")) : 512);
   a->nseg = nchunks > 0 ? (nchunks + a->spc - 1) / a->spc : 1;
 }
 
@@ -822,7 +928,7 @@ hipError_t segment_states(const GatedArgs& a, int sides, hipStream_t s) {
   fn<<<dim3(chains * a.nseg, sides), dim3(4 * D), bytes, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  gl_scan_kernel<D><<<dim3(static_cast<unsigned>((static_cast<long long>(chains) * (D * D / 4) + 255) / 256), sides), dim3(256), 0, s>>>(a);
+  gl_scan_kernel<D><<<dim3(chains * (D * D / 256), sides), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 

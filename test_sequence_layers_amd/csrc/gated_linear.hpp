@@ -21,6 +21,7 @@ struct GlDecays {
   float e[kGlChunk];                 // e_s (0 past the sequence)
   float from[kGlChunk];              // exp(b_u): from the chunk's start
   float to[kGlChunk];                // exp(b_C - b_s): to the chunk's end
+  float to_e[kGlChunk];              // the same times e_s
   float whole[4];                    // exp(b_C) (first entry)
 };
 
@@ -29,23 +30,45 @@ struct GlDecays {
 // tokens after a forgotten one (g = -inf, or the type's lowest value) keep exact differences.
 constexpr double kGlNever = -4096.0;
 
+// two floats rounded to bf16 in one word, and the floats that a word holds
+__device__ __forceinline__ uint32_t gl_pack(float lo, float hi) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{lo, hi}, b2));
+}
+__device__ __forceinline__ float gl_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float gl_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+
+// x of the lane `kCtrl` names (row_shr within 16 lanes, or the broadcast of a row's last lane to
+// the rows of the mask), 0 where there is none
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double gl_dpp(double x) {
+  typedef int pair __attribute__((ext_vector_type(2)));
+  pair y = __builtin_bit_cast(pair, x);
+  const int lo = __builtin_amdgcn_update_dpp(0, y[0], kCtrl, kRows, 0xF, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, y[1], kCtrl, kRows, 0xF, false);
+  return __builtin_bit_cast(double, pair{lo, hi});
+}
+
 // One wave, lane = token: g is the token's log decay (0 past the sequence).  The prefix sum
 // runs in 64 bits: b_u - b_s is a small difference of sums that may be large.
 __device__ __forceinline__ void gl_decays(float g, float e, GlDecays* d, int lane) {
   double x = static_cast<double>(g) * 1.4426950408889634;
   if (x < kGlNever) x = kGlNever;  // a NaN stays one
-#pragma unroll
-  for (int o = 1; o < kGlChunk; o <<= 1) {
-    const double y = __shfl_up(x, o, 64);
-    if (lane >= o) x += y;
-  }
+  x += gl_dpp<0x111, 0xF>(x);  // row_shr 1, 2, 4, 8: sums of 16 lanes
+  x += gl_dpp<0x112, 0xF>(x);
+  x += gl_dpp<0x114, 0xF>(x);
+  x += gl_dpp<0x118, 0xF>(x);
+  x += gl_dpp<0x142, 0xA>(x);  // row_bcast 15 into rows 1 and 3, row_bcast 31 into rows 2 and 3
+  x += gl_dpp<0x143, 0xC>(x);
   const double last = __shfl(x, kGlChunk - 1, 64);
-  const float h = static_cast<float>(x);
+  const float h = static_cast<float>(x), to = __builtin_amdgcn_exp2f(static_cast<float>(last - x));
   d->bh[lane] = h;
   d->bl[lane] = static_cast<float>(x - h);
   d->e[lane] = e;
   d->from[lane] = __builtin_amdgcn_exp2f(h);
-  d->to[lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - x));
+  d->to[lane] = to;
+  d->to_e[lane] = to * e;
   if (lane == 0) d->whole[0] = __builtin_amdgcn_exp2f(static_cast<float>(last));
 }
 
@@ -62,8 +85,10 @@ typedef uint32_t gl_u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t gl_u4 __attribute__((ext_vector_type(4)));
 
 // Loads and stores through buffer resources whose range ends at the last valid token: rows
-// past it read as zero and their stores are dropped.
+// past it read as zero and their stores are dropped.  The range is the same in every lane; said
+// so, it stays in scalar registers (else each access is wrapped in a loop over the lanes' values).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t gl_span(const void* base, int bytes) {
+  bytes = __builtin_amdgcn_readfirstlane(bytes);
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes > 0 ? bytes : 0, 0x00020000);
 }
 

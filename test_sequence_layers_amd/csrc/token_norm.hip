@@ -24,25 +24,25 @@ namespace {
 enum { kLayer = 0, kRms = 1, kL2 = 2 };
 enum { kActNone = 0, kSilu = 1, kGelu = 2, kSigmoid = 3 };
 
-// W consecutive elements (16 bytes, or one)
+// W consecutive elements (16 bytes, or one) as they are loaded
+template <typename IO, int W>
+struct Vec {
+  typedef IO type __attribute__((ext_vector_type(W)));
+  type v;
+  __device__ __forceinline__ void load(const IO* p) {
+    if constexpr (W == 1) v[0] = p[0];
+    else v = *reinterpret_cast<const type*>(p);
+  }
+  __device__ __forceinline__ void widen(float* x, bool have) const {
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = have ? to_f32(static_cast<IO>(v[i])) : 0.0f;
+  }
+};
 template <typename IO, int W>
 __device__ __forceinline__ void load_vec(const IO* p, float* x) {
-  if constexpr (W == 1) {
-    x[0] = to_f32(p[0]);
-  } else {
-    if constexpr (W == 4) {
-      const gl_f4 y = *reinterpret_cast<const gl_f4*>(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = y[i];
-    } else {
-      const gl_u4 y = *reinterpret_cast<const gl_u4*>(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __builtin_bit_cast(float, y[i] << 16);
-        x[2 * i + 1] = __builtin_bit_cast(float, y[i] & 0xFFFF0000u);
-      }
-    }
-  }
+  Vec<IO, W> v;
+  v.load(p);
+  v.widen(x, true);
 }
 template <typename IO, int W>
 __device__ __forceinline__ void store_vec(IO* p, const float* x) {
@@ -205,8 +205,8 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
   constexpr int RB = Block<LPR>::kRows, N = NV * W;
   const int in_row = threadIdx.x % LPR, group = threadIdx.x / LPR;
   const int head = blockIdx.y;
-  const long long all = static_cast<long long>(a.B) * a.T;
-  const long long from = all * blockIdx.x / gridDim.x, to = all * (blockIdx.x + 1) / gridDim.x;
+  const long long all = static_cast<long long>(a.B) * a.T;  // at most 2^30
+  const int from = static_cast<int>(all * blockIdx.x / gridDim.x), to = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
   const IO* xp = static_cast<const IO*>(a.x);
   const IO* gp = static_cast<const IO*>(a.gate);
   const IO* dyp = static_cast<const IO*>(a.dy);
@@ -216,40 +216,68 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
   float sw[N], sb[N], ss[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) sw[i] = sb[i] = ss[i] = 0.0f;
-  for (long long first = from; first < to; first += RB) {
-    const long long i0 = first + group;
-    const bool live = i0 < to;
-    const long long bt = live ? i0 : from;
-    const size_t base = (static_cast<size_t>(bt / a.T * a.H + head) * a.T + bt % a.T) * a.d;
+  // a row as it is loaded; that of the next turn is on its way while one is worked on
+  struct Row {
+    Vec<IO, W> x[NV], dy[NV], gt[NV];
+    size_t base;
+    bool live;
+  } next;
+  auto fetch = [&](int first) {
+    next.live = first + group < to;
+    const unsigned bt = next.live ? first + group : 0, b = bt / static_cast<unsigned>(a.T);  // a valid row in any case
+    next.base = (static_cast<size_t>(b * static_cast<unsigned>(a.H) + head) * a.T + (bt - b * static_cast<unsigned>(a.T))) * a.d;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (v * LPR + in_row) * W, col = at < a.d ? at : 0;
+      next.x[v].load(xp + next.base + col);
+      next.dy[v].load(dyp + next.base + col);
+      if (gp) next.gt[v].load(gp + next.base + col);
+    }
+  };
+  if (from < to) fetch(from);
+  // the head's parameters, kept in registers while they are few
+  constexpr bool kKeep = N <= 16;
+  float wt_[kKeep ? N : W], bs_[kKeep ? N : W], sc_[kKeep ? N : W];
+  auto parameters = [&](int col, float* wt, float* bs, float* sc) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      wt[i] = sc[i] = 1.0f;
+      bs[i] = 0.0f;
+    }
+    if (a.weight) load_par<W>(a.weight + hb + col, wt);
+    if (a.bias) load_par<W>(a.bias + hb + col, bs);
+    if (a.scale) load_par<W>(a.scale + hb + col, sc);
+  };
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (v * LPR + in_row) * W;
+      parameters(at < a.d ? at : 0, wt_ + v * W, bs_ + v * W, sc_ + v * W);
+    }
+  }
+  for (int first = from; first < to; first += RB) {
+    const size_t base = next.base;
     float x[N], dy[N], gt[N];
     bool have[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int col = (v * LPR + in_row) * W;
-      have[v] = live && col < a.d;
-#pragma unroll
-      for (int i = 0; i < W; ++i) x[v * W + i] = dy[v * W + i] = gt[v * W + i] = 0.0f;
-      if (have[v]) {
-        load_vec<IO, W>(xp + base + col, x + v * W);
-        load_vec<IO, W>(dyp + base + col, dy + v * W);
-        if (gp) load_vec<IO, W>(gp + base + col, gt + v * W);
-      }
+      have[v] = next.live && (v * LPR + in_row) * W < a.d;
+      next.x[v].widen(x + v * W, have[v]);
+      next.dy[v].widen(dy + v * W, have[v]);
+      if (gp) next.gt[v].widen(gt + v * W, have[v]);
     }
+    if (first + RB < to) fetch(first + RB);
     const float r = normalise<LPR, N>(x, have, W, a.kind, a.d, a.eps, red, &turn);
     float m1 = 0.0f, m2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (!have[v]) continue;
       const int col = (v * LPR + in_row) * W;
-      float wt[W], bs[W], sc[W], dg[W];
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        wt[i] = sc[i] = 1.0f;
-        bs[i] = 0.0f;
-      }
-      if (a.weight) load_par<W>(a.weight + hb + col, wt);
-      if (a.bias) load_par<W>(a.bias + hb + col, bs);
-      if (a.scale) load_par<W>(a.scale + hb + col, sc);
+      float* wt = wt_ + (kKeep ? v * W : 0);
+      float* bs = bs_ + (kKeep ? v * W : 0);
+      float* sc = sc_ + (kKeep ? v * W : 0);
+      float dg[W];
+      if constexpr (!kKeep) parameters(col, wt, bs, sc);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const int j = v * W + i;
@@ -329,24 +357,28 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
   }
 }
 
-// out[head][col] = sum over the parts, in order (64 bits): 64 columns a workgroup, four
-// quarters of the parts each, joined through LDS.
-__global__ __launch_bounds__(256) void norm_sum_kernel(NormArgs a, const float* part, int parts) {
-  __shared__ double quarter[4][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+// out[head][col] = sum over the parts (64 bits): a workgroup takes 32 columns, 32 groups of threads
+// a share of the parts each, joined through LDS in order.  Few long columns (H = 1) are bound by the
+// loads' latency, so the shares are short.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs a, const float* part, int parts) {
+  __shared__ double share[32][33];
+  const int c = threadIdx.x & 31, q = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
   const int head = blockIdx.y, which = blockIdx.z;
   float* out = which == 0 ? a.dweight : which == 1 ? a.dbias : a.dscale;
   if (!out) return;
   double s = 0.0;
   if (col < a.d) {
     const float* p = part + static_cast<size_t>(head) * parts * 3 * a.d + static_cast<size_t>(which) * a.d + col;
-    for (int i = parts * q / 4; i < parts * (q + 1) / 4; ++i) s += p[static_cast<size_t>(i) * 3 * a.d];
+#pragma unroll 8
+    for (int i = q; i < parts; i += 32) s += p[static_cast<size_t>(i) * 3 * a.d];
   }
-  quarter[q][threadIdx.x & 63] = s;
+  share[q][c] = s;
   __syncthreads();
-  if (q == 0 && col < a.d)
-    out[static_cast<size_t>(head) * a.d + col] =
-        static_cast<float>((quarter[0][threadIdx.x] + quarter[1][threadIdx.x]) + (quarter[2][threadIdx.x] + quarter[3][threadIdx.x]));
+  if (q == 0 && col < a.d) {
+#pragma unroll
+    for (int i = 1; i < 32; ++i) s += share[i][c];
+    out[static_cast<size_t>(head) * a.d + col] = static_cast<float>(s);
+  }
 }
 
 // 16-byte vectors need whole vectors in a row and aligned tensors and parameters
@@ -427,7 +459,7 @@ hipError_t bwd_io(const NormArgs& a, void* ws, hipStream_t s) {
   constexpr int W = 16 / static_cast<int>(sizeof(IO));
   hipError_t e = vectors(a, sizeof(IO)) ? layout<W>(a.d, go) : layout<1>(a.d, go);
   if (e != hipSuccess || !(a.dweight || a.dbias || a.dscale)) return e;
-  norm_sum_kernel<<<dim3((a.d + 63) / 64, a.H, 3), dim3(256), 0, s>>>(a, static_cast<const float*>(ws), bwd_parts(a.B, a.H, a.T));
+  norm_sum_kernel<<<dim3((a.d + 31) / 32, a.H, 3), dim3(1024), 0, s>>>(a, static_cast<const float*>(ws), bwd_parts(a.B, a.H, a.T));
   return hipGetLastError();
 }
 
