@@ -35,10 +35,28 @@ __device__ __forceinline__ gl_f4 keep4(float f, const gl_f4& x) {
 __device__ __forceinline__ float dot4(const gl_f4& a, const gl_f4& b) {
   return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
 }
-// over the four lanes (g) that share r
+// over the four lanes (g) that share r: v_permlane32_swap and v_permlane16_swap of x with itself
+// leave the two halves' (rows') values side by side in two registers
 __device__ __forceinline__ float over_g(float x) {
-  x += __shfl_xor(x, 16, 64);
-  return x + __shfl_xor(x, 32, 64);
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t a0 = h[0], a1 = h[1];
+  const uint32_t v = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a0) + __builtin_bit_cast(float, a1));
+  const auto w = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  const uint32_t b0 = w[0], b1 = w[1];
+  return __builtin_bit_cast(float, b0) + __builtin_bit_cast(float, b1);
+}
+
+// over the sixteen lanes (r) that share g, by rotations within the row
+template <int kShift>
+__device__ __forceinline__ float rotate(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + kShift, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float over_r(float x) {
+  x += rotate<8>(x);
+  x += rotate<4>(x);
+  x += rotate<2>(x);
+  return x + rotate<1>(x);
 }
 
 // Matrices in LDS hold a token (or a row of token pairs) per row.  Math<IO>: their element and
@@ -88,6 +106,11 @@ struct Math<float> {
     return mma<false>(a, along<false>(row, p, g), c);
   }
   template <int D> static __device__ __forceinline__ gl_f4 row4(const float* row, int cb, int g) { return at4(row, 16 * cb + 4 * g); }
+  typedef gl_f4 Four;  // four features of a token, from element `elem` of the source
+  static __device__ __forceinline__ Four load4(__amdgpu_buffer_rsrc_t src, int elem) {
+    return __builtin_bit_cast(gl_f4, __builtin_amdgcn_raw_buffer_load_b128(src, elem * 4, 0, 0));
+  }
+  static __device__ __forceinline__ gl_f4 widen4(const Four& x) { return x; }
   static __device__ __forceinline__ void store4(const gl_f4& x, __amdgpu_buffer_rsrc_t dst, int elem) {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(gl_u4, x), dst, elem * 4, 0, 0);
   }
@@ -175,9 +198,13 @@ struct Math<bf16> {
     return mma<false>(a, along<false>(row, p, g), c);
   }
   template <int D> static __device__ __forceinline__ gl_f4 row4(const bf16* row, int cb, int g) {
-    const gl_u2 w = *reinterpret_cast<const gl_u2*>(row + 16 * cb + 4 * g);
-    return gl_f4{gl_lo(w[0]), gl_hi(w[0]), gl_lo(w[1]), gl_hi(w[1])};
+    return widen4(*reinterpret_cast<const gl_u2*>(row + 16 * cb + 4 * g));
   }
+  typedef gl_u2 Four;
+  static __device__ __forceinline__ Four load4(__amdgpu_buffer_rsrc_t src, int elem) {
+    return __builtin_amdgcn_raw_buffer_load_b64(src, elem * 2, 0, 0);
+  }
+  static __device__ __forceinline__ gl_f4 widen4(const Four& w) { return gl_f4{gl_lo(w[0]), gl_hi(w[0]), gl_lo(w[1]), gl_hi(w[1])}; }
   static __device__ __forceinline__ void store4(const gl_f4& x, __amdgpu_buffer_rsrc_t dst, int elem) {
     const gl_u2 y = {gl_pack(x[0], x[1]), gl_pack(x[2], x[3])};
     __builtin_amdgcn_raw_buffer_store_b64(y, dst, elem * 2, 0, 0);
@@ -197,7 +224,6 @@ struct Shape {
   static constexpr int kTile = kC * kLd;
   static constexpr int kLdP = kC + Math<IO>::kPad;             // row pitch of a factor of token pairs
   static constexpr int kPlane = kC * kLdP;
-  static constexpr int kVec = static_cast<int>(sizeof(IO));    // 16-byte vectors of a tile per thread
 };
 
 // Loads.  A tile's registers are filled by buffer loads whose range ends at the last valid token
@@ -206,19 +232,20 @@ struct Shape {
 // them, as long as their number is known.  So the stores of a chunk are the same on every path
 // too (lanes or waves with nothing to store have an empty range), and `no_store` stands in for those
 // of the chunk before the first.
-template <typename IO, int D>
+template <typename IO, int D, int kThreads = 4 * D>
 struct Tile {
-  gl_u4 x[sizeof(IO)];
+  static constexpr int kVec = 4 * D * static_cast<int>(sizeof(IO)) / kThreads;  // 16-byte vectors a thread
+  gl_u4 x[kVec];
   // tokens c0 .. of base, `rows` of them valid (may be negative)
   __device__ __forceinline__ void load(const IO* base, long long c0, int rows, int tid) {
     const __amdgpu_buffer_rsrc_t src = gl_span(base + c0 * D, max(0, min(kC, rows)) * D * static_cast<int>(sizeof(IO)));
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(IO)); ++i)
-      x[i] = __builtin_amdgcn_raw_buffer_load_b128(src, (tid + i * 4 * D) * 16, 0, 0);
+    for (int i = 0; i < kVec; ++i)
+      x[i] = __builtin_amdgcn_raw_buffer_load_b128(src, (tid + i * kThreads) * 16, 0, 0);
   }
   __device__ __forceinline__ void put(typename Math<IO>::Elem* m, int tid) const {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(IO)); ++i) Math<IO>::template put_vec<D>(m, tid + i * 4 * D, x[i]);
+    for (int i = 0; i < kVec; ++i) Math<IO>::template put_vec<D>(m, tid + i * kThreads, x[i]);
   }
 };
 __device__ __forceinline__ void store1(float x, __amdgpu_buffer_rsrc_t dst, int i) {
@@ -470,6 +497,14 @@ __global__ __launch_bounds__(256) void gl_scan_kernel(GatedArgs a) {
   }
 }
 
+// The state at the segment's start (side 0) or its gradient at the segment's end (side 1).
+template <int D>
+__device__ __forceinline__ const float* segment_state(const GatedArgs& a, int side, int chain, int seg) {
+  if (a.nseg > 1) return (side == 0 ? a.seg_w : a.seg_g) + (static_cast<size_t>(chain) * a.nseg + seg) * (D * D);
+  if (side == 0) return initial_state(a, chain, D * D);
+  return a.dw_out ? a.dw_out + static_cast<size_t>(chain) * (D * D) : nullptr;
+}
+
 // ---------------------------------------------------------------- forward
 template <typename IO, int D>
 struct FwdLds {
@@ -496,7 +531,7 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
   const int nchunks = (T + kC - 1) / kC, first = seg * a.spc, end = min(nchunks, first + a.spc);
 
   gl_f4 w[NW];  // W^T: W's rows 16 wv + r
-  load_state<D, true>(w, a.nseg > 1 ? a.seg_w + static_cast<size_t>(blockIdx.x) * D * D : initial_state(a, chain, D * D), wv, g, r);
+  load_state<D, true>(w, segment_state<D>(a, 0, chain, seg), wv, g, r);
   // what a chunk's step needs in registers: its tiles, and the gates of the chunk after it
   struct Set {
     Tile<IO, D> q, k, v;
@@ -582,9 +617,9 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
 //   dv_s = e_s x_s,  x_s = sum_{u >= s} exp(b_u - b_s) (q_u . k_s) dz_u + exp(b_C - b_s) G k_s,
 //   dk_s = e_s (sum_{u >= s} exp(b_u - b_s) (dz_u . v_s) q_u + exp(b_C - b_s) G^T v_s),
 //   de_s = v_s . x_s,
-// W the state before the chunk, G the gradient at its end.  Two roles share no data: one
-// workgroup walks a segment forward with W for dq, another walks it backward with G for dk and
-// dv.  So no state is stored on the way.
+// W the state before the chunk, G the gradient at its end.  gl_dq_kernel walks a segment forward
+// with W for dq, gl_dkv_kernel walks it backward with G for dk and dv.  So no state is stored on
+// the way.
 //
 // dg_t = a_t <G_t, W_{t-1}> is the sum over the pairs (s, u), s < t <= u, of what token s
 // contributes to output u.  With m_us = exp(b_u - b_s) e_s (q_u . k_s)(dz_u . v_s), per chunk:
@@ -593,268 +628,318 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
 //   in_u = exp(b_u) dz_u . W q_u,  out_s = exp(b_C - b_s) e_s v_s . G k_s,  past = exp(b_C) <G, W>.
 // Only the row - col sums cancel, over one chunk; nothing grows with the sequence.  `past` follows
 // from <G, W> at the segment's end: past_c = <G, W>_end(c) - sum out, <G, W>_start(c) = past_c +
-// sum in.  The two roles store row, in, col, out per token, and gl_dgate_kernel adds them.
+// sum in.  The two kernels store row, in, col, out per token, and gl_dgate_kernel adds them.
 template <typename IO, int D>
-struct BwdLds {
+struct DqLds {
   typedef Shape<IO, D> S;
-  typename S::Elem q[S::kTile], k[S::kTile], v[S::kTile], z[S::kTile];
-  typename S::Elem p[Math<IO>::kPlanes * S::kPlane], r[Math<IO>::kPlanes * S::kPlane];
-  float part[S::kNW][kC];  // in_u or out_s, the waves' shares
-  float pairs[4][kC];      // row_u or col_s, the blocks' shares
-  float diag[kC];          // m_ss
-  GlDecays dec[2];  // of this chunk and the next
+  typename S::Elem k[S::kTile], v[S::kTile], z[S::kTile];
+  typename S::Elem r[Math<IO>::kPlanes * S::kPlane];
+  float part[S::kNW][kC];  // in_u, the waves' shares
+  GlDecays dec[2];         // of this chunk and the next
 };
 
 template <typename IO, int D>
-__global__ __launch_bounds__(4 * D) void gl_bwd_kernel(GatedArgs a) {
+__global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
   typedef Math<IO> M;
   typedef Shape<IO, D> S;
   constexpr int NW = S::kNW, LD = S::kLd, LDP = S::kLdP;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
-  BwdLds<IO, D>& L = *reinterpret_cast<BwdLds<IO, D>*>(lds_raw);
+  DqLds<IO, D>& L = *reinterpret_cast<DqLds<IO, D>*>(lds_raw);
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // the two roles of a segment are 8 workgroups apart: the same XCD, so one L2 serves both
-  const int item = (blockIdx.x >> 4) * 8 + (blockIdx.x & 7), role = (blockIdx.x >> 3) & 1;
-  if (item >= a.B * a.H * a.nseg) return;
-  const int chain = item / a.nseg, seg = item % a.nseg, T = a.T;
+  const int chain = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg, T = a.T;
   const Seq s = sequence(a, chain);
   const IO* q = static_cast<const IO*>(a.q) + s.row0 * D;
   const IO* k = static_cast<const IO*>(a.k) + s.row0 * D;
   const IO* v = static_cast<const IO*>(a.v) + s.row0 * D;
   const IO* dz = static_cast<const IO*>(a.dz) + s.row0 * D;
+  IO* dq = static_cast<IO*>(a.dq) + s.row0 * D;
   const int nchunks = (T + kC - 1) / kC, first = seg * a.spc, end = min(nchunks, first + a.spc);
   const size_t rows_all = static_cast<size_t>(a.B) * a.H * T;
-  float* row_o = a.ws_tok ? a.ws_tok + s.row0 : nullptr;
-  float* in_o = a.ws_tok ? row_o + rows_all : nullptr;
-  float* col_o = a.ws_tok ? in_o + rows_all : nullptr;
-  float* out_o = a.ws_tok ? col_o + rows_all : nullptr;
-  // the gradient of the state at the segment's end
-  const float* g_end = a.nseg > 1 ? a.seg_g + static_cast<size_t>(item) * D * D
-                                  : a.dw_out ? a.dw_out + static_cast<size_t>(chain) * D * D : nullptr;
+  float* in_o = a.ws_tok ? a.ws_tok + s.row0 + rows_all : nullptr;
 
   // what a chunk's step needs in registers: its tiles, and the gates of the chunk after it
   struct Set {
-    Tile<IO, D> q, k, v, z;
+    Tile<IO, D> k, v, z;
     GateRate gr;
   } y;
-  auto fetch = [&](int c, int next) {
+  auto fetch = [&](int c) {
     const long long c0 = static_cast<long long>(c) * kC;
-    y.gr.load(s, static_cast<long long>(next) * kC, lane);
-    const int valid = c >= first && c < end ? s.len - static_cast<int>(c0) : 0;
-    y.q.load(q, c0, valid, tid);
+    y.gr.load(s, c0 + kC, lane);
+    const int valid = c < end ? s.len - static_cast<int>(c0) : 0;
     y.k.load(k, c0, valid, tid);
     y.v.load(v, c0, valid, tid);
     y.z.load(dz, c0, valid, tid);
   };
   const bool decayer = wv == NW - 1;  // the wave that forms the next chunk's decays
-  // tiles of chunk c to LDS, those of `next` on their way, its decays formed
-  auto stage = [&](int c, int next, int after, int turn) {
-    gl_barrier();  // the previous chunk's tiles have been read
+  // in_u of a chunk whose shares are in LDS, stored by wave 0 (c < first: nothing)
+  auto flush = [&](int c) {
+    float in = 0.0f;
+#pragma unroll
+    for (int x = 0; x < NW; ++x) in += L.part[x][lane];
+    store1(in, gl_span(in_o + c * kC, in_o && wv == 0 && c >= first ? min(kC, T - c * kC) * 4 : 0), lane);
+  };
+
+  gl_f4 w[NW];  // W's columns 16 wv + r
+  {
+    GateRate gr;
+    gr.load(s, static_cast<long long>(first) * kC, lane);
+    fetch(first);
+    no_store<5>();
+    if (decayer) gr.decays(s, a.eta, static_cast<long long>(first) * kC, &L.dec[0], lane);
+  }
+  load_state<D, false>(w, segment_state<D>(a, 0, chain, seg), wv, g, r);
+  zero_unused<IO, D, true>(L.r, wv, g, r);
+  for (int c = first; c < end; ++c) {
+    const int c0 = c * kC, turn = (c - first) & 1;
+    const GlDecays& dec = L.dec[turn];
+    gl_barrier();  // the previous chunk's tiles have been read, its sums are whole
+    flush(c - 1);
+    y.k.put(L.k, tid);
+    y.v.put(L.v, tid);
+    y.z.put(L.z, tid);
+    const GateRate gr = y.gr;
+    // the wave's features of Q, for in_u
+    typename M::Four qu[4];
+    const __amdgpu_buffer_rsrc_t qsrc = gl_span(q + static_cast<size_t>(c0) * D, in_o ? max(0, min(kC, s.len - c0)) * D * static_cast<int>(sizeof(IO)) : 0);
+#pragma unroll
+    for (int ut = 0; ut < 4; ++ut) qu[ut] = M::load4(qsrc, (16 * ut + r) * D + 16 * wv + 4 * g);
+    gl_barrier();
+    fetch(c + 1);
+    if (decayer && c + 1 < end) gr.decays(s, a.eta, static_cast<long long>(c + 1) * kC, &L.dec[turn ^ 1], lane);
+    wave_blocks<NW>(wv, [&](auto n, int first_block) {
+      constexpr int N = n.value;
+      gl_f4 rd[N];
+      int ut[N], st[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        ut[i] = block_row(first_block + i * NW);
+        st[i] = first_block + i * NW - ut[i] * (ut[i] + 1) / 2;
+        rd[i] = row_products<IO, D>(L.v + (16 * st[i] + r) * LD, L.z + (16 * ut[i] + r) * LD, g);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int u = 16 * ut[i] + r, s4 = 16 * st[i] + 4 * g;
+        const float uh = dec.bh[u], ul = dec.bl[u];
+        const gl_f4 sh = at4(dec.bh, s4), sl = at4(dec.bl, s4), e = at4(dec.e, s4);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) rd[i][x] = s4 + x <= u ? rd[i][x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) M::put(L.r + (16 * ut[i] + r) * LDP, S::kPlane, st[i], g, rd[i]);
+    });
+    gl_barrier();
+    typename M::Op kf[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) kf[p] = M::template down<D>(L.k, LD, p, wv, g, r);
+    typename M::template Parts<3> wp[S::kNP];
+    split_state<IO, D, 3>(wp, w);
+    const __amdgpu_buffer_rsrc_t dst = gl_span(dq + static_cast<size_t>(c0) * D, min(kC, T - c0) * D * static_cast<int>(sizeof(IO)));
+#pragma unroll
+    for (int ut = 0; ut < 4; ++ut) {
+      const int u = 16 * ut + r;
+      const gl_f4 xi = keep4(dec.from[u], state_times<IO, D, 3>(wp, L.z + u * LD, g));
+      gl_f4 xp = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int p = 0; p <= ut / 2; ++p) xp = M::mma_planes(kf[p], L.r + u * LDP, S::kPlane, p, g, xp);
+      const float in = over_g(dot4(M::widen4(qu[ut]), xi));
+      if (g == 0) L.part[wv][u] = in;
+      M::store4(xi + xp, dst, u * D + 16 * wv + 4 * g);
+    }
+    update_state<IO, D, 3>(w, dec.whole[0], L.v, kf, dec.to_e, g, r);
+  }
+  gl_barrier();
+  flush(end - 1);
+  if (in_o) {  // <G, W> at the segment's end
+    gl_f4 ge[NW];
+    load_state<D, false>(ge, segment_state<D>(a, 1, chain, seg), wv, g, r);
+    double x = 0.0;
+#pragma unroll
+    for (int b = 0; b < NW; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x += static_cast<double>(w[b][e]) * ge[b][e];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
+    if (lane == 0) a.ws_end[static_cast<size_t>(blockIdx.x) * NW + wv] = x;
+  }
+}
+
+// Two waves for each 16 columns: one group has G^T's columns for dv, the other G's for dk.
+template <typename IO, int D>
+struct DkvLds {
+  typedef Shape<IO, D> S;
+  typename S::Elem q[S::kTile], k[S::kTile], v[S::kTile], z[S::kTile];
+  typename S::Elem p[Math<IO>::kPlanes * S::kPlane], r[Math<IO>::kPlanes * S::kPlane];
+  float part[S::kNW][kC];  // v_s . G k_s to the chunk's end, the waves' shares
+  float pairs[4][kC];      // col_s / e_s, the blocks' shares
+  float rows[4][kC];       // row_u, the blocks' shares
+  float diag[kC];          // m_ss / e_s
+  GlDecays dec[2];         // of this chunk and the next
+};
+
+template <typename IO, int D>
+__global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
+  typedef Math<IO> M;
+  typedef Shape<IO, D> S;
+  constexpr int NW = S::kNW, LD = S::kLd, LDP = S::kLdP;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+  DkvLds<IO, D>& L = *reinterpret_cast<DkvLds<IO, D>*>(lds_raw);
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wv = wave % NW;
+  const bool dk_group = wave >= NW;
+  const int chain = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg, T = a.T;
+  const Seq s = sequence(a, chain);
+  const IO* q = static_cast<const IO*>(a.q) + s.row0 * D;
+  const IO* k = static_cast<const IO*>(a.k) + s.row0 * D;
+  const IO* v = static_cast<const IO*>(a.v) + s.row0 * D;
+  const IO* dz = static_cast<const IO*>(a.dz) + s.row0 * D;
+  IO* out = static_cast<IO*>(dk_group ? a.dk : a.dv) + s.row0 * D;
+  float* de_o = a.deta_tok ? a.deta_tok + s.row0 : nullptr;
+  const int nchunks = (T + kC - 1) / kC, first = seg * a.spc, end = min(nchunks, first + a.spc);
+  const size_t rows_all = static_cast<size_t>(a.B) * a.H * T;
+  float* col_o = a.ws_tok ? a.ws_tok + s.row0 + 2 * rows_all : nullptr;
+  float* out_o = a.ws_tok ? col_o + rows_all : nullptr;
+  float* row_o = a.ws_tok ? a.ws_tok + s.row0 : nullptr;
+
+  // what a chunk's step needs in registers: its tiles, and the gates of the chunk before it
+  struct Set {
+    Tile<IO, D, 8 * D> q, k, v, z;
+    GateRate gr;
+  } y;
+  auto fetch = [&](int c) {
+    const long long c0 = static_cast<long long>(c) * kC;
+    y.gr.load(s, c0 - kC, lane);
+    const int valid = c >= first ? s.len - static_cast<int>(c0) : 0;
+    y.q.load(q, c0, valid, tid);
+    y.k.load(k, c0, valid, tid);
+    y.v.load(v, c0, valid, tid);
+    y.z.load(dz, c0, valid, tid);
+  };
+  const bool decayer = wave == 2 * NW - 1;  // the wave that forms the next chunk's decays
+  // sums of a chunk whose shares are in LDS, stored by wave 0 (c >= end: nothing)
+  auto flush = [&](int c, const float* es) {
+    const int c0 = c * kC, bytes = wave == 0 && c < end ? min(kC, T - c0) * 4 : 0;
+    float o = 0.0f, col = 0.0f, row = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) o += L.part[i][lane];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      row += t <= lane >> 4 ? L.rows[t][lane] : 0.0f;
+      col += t >= lane >> 4 ? L.pairs[t][lane] : 0.0f;
+    }
+    const float e = es[lane];
+    store1(c0 + lane < s.len ? a.eta * (col + L.diag[lane] + o) : 0.0f, gl_span(de_o + c0, de_o ? bytes : 0), lane);
+    const int sums = a.ws_tok ? bytes : 0;
+    store1(e * col, gl_span(col_o + c0, sums), lane);
+    store1(e * o, gl_span(out_o + c0, sums), lane);
+    store1(row, gl_span(row_o + c0, sums), lane);
+  };
+
+  gl_f4 x[NW];  // G's rows 16 wv + r (dv) or its columns (dk)
+  if (first < end) {
+    GateRate gr;
+    gr.load(s, static_cast<long long>(end - 1) * kC, lane);
+    fetch(end - 1);
+    no_store<8>();
+    if (decayer) gr.decays(s, a.eta, static_cast<long long>(end - 1) * kC, &L.dec[0], lane);
+  }
+  if (dk_group) load_state<D, false>(x, segment_state<D>(a, 1, chain, seg), wv, g, r);
+  else load_state<D, true>(x, segment_state<D>(a, 1, chain, seg), wv, g, r);
+  zero_unused<IO, D, false>(L.p, wave, g, r);
+  zero_unused<IO, D, false>(L.r, wave, g, r);
+  for (int c = end - 1; c >= first; --c) {
+    const int c0 = c * kC, turn = (end - 1 - c) & 1;
+    const GlDecays& dec = L.dec[turn];
+    gl_barrier();  // the previous chunk's tiles have been read, its sums are whole
+    flush(c + 1, L.dec[turn ^ 1].e);
     y.q.put(L.q, tid);
     y.k.put(L.k, tid);
     y.v.put(L.v, tid);
     y.z.put(L.z, tid);
     const GateRate gr = y.gr;
     gl_barrier();
-    fetch(next, after);
-    if (decayer && next >= first && next < end) gr.decays(s, a.eta, static_cast<long long>(next) * kC, &L.dec[turn ^ 1], lane);
-  };
-  auto begin = [&](int c, int next) {
-    GateRate gr;
-    gr.load(s, static_cast<long long>(c) * kC, lane);
-    fetch(c, next);
-    if (decayer) gr.decays(s, a.eta, static_cast<long long>(c) * kC, &L.dec[0], lane);
-  };
-  // per-token sums are stored by wave 0
-  auto per_token = [&](float* p, int c0) { return gl_span(p + c0, p && wv == 0 ? min(kC, T - c0) * 4 : 0); };
-
-  if (role == 0) {
-    gl_f4 w[NW];  // W's columns 16 wv + r
-    load_state<D, false>(w, a.nseg > 1 ? a.seg_w + static_cast<size_t>(item) * D * D : initial_state(a, chain, D * D), wv, g, r);
-    IO* dq = static_cast<IO*>(a.dq) + s.row0 * D;
-    begin(first, first + 1);
-    no_store<6>();
-    zero_unused<IO, D, true>(L.r, wv, g, r);
-    for (int c = first; c < end; ++c) {
-      const int c0 = c * kC, turn = (c - first) & 1;
-      const GlDecays& dec = L.dec[turn];
-      stage(c, c + 1, c + 2, turn);
-      wave_blocks<NW>(wv, [&](auto n, int first_block) {
-        constexpr int N = n.value;
-        gl_f4 rd[N], p[N];
-        int ut[N], st[N];
+    fetch(c - 1);
+    if (decayer && c > first) gr.decays(s, a.eta, static_cast<long long>(c - 1) * kC, &L.dec[turn ^ 1], lane);
+    // rows s of P^T and R^T (decayed, without e_s)
+    wave_blocks<2 * NW>(wave, [&](auto n, int first_block) {
+      constexpr int N = n.value;
+      gl_f4 p[N], rd[N];
+      int ut[N], st[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          ut[i] = block_row(first_block + i * NW);
-          st[i] = first_block + i * NW - ut[i] * (ut[i] + 1) / 2;
-          rd[i] = row_products<IO, D>(L.v + (16 * st[i] + r) * LD, L.z + (16 * ut[i] + r) * LD, g);
-          if (row_o) p[i] = row_products<IO, D>(L.k + (16 * st[i] + r) * LD, L.q + (16 * ut[i] + r) * LD, g);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int u = 16 * ut[i] + r, s4 = 16 * st[i] + 4 * g;
-          const float uh = dec.bh[u], ul = dec.bl[u];
-          const gl_f4 sh = at4(dec.bh, s4), sl = at4(dec.bl, s4), e = at4(dec.e, s4);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) rd[i][x] = s4 + x <= u ? rd[i][x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
-          if (row_o) {
-            float row = 0.0f;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) row += s4 + x < u ? p[i][x] * rd[i][x] : 0.0f;
-            row = over_g(row);
-            if (g == 0) L.pairs[st[i]][u] = row;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) M::put(L.r + (16 * ut[i] + r) * LDP, S::kPlane, st[i], g, rd[i]);
-      });
-      gl_barrier();
-      typename M::Op kf[2];
-#pragma unroll
-      for (int p = 0; p < 2; ++p) kf[p] = M::template down<D>(L.k, LD, p, wv, g, r);
-      typename M::template Parts<3> wp[S::kNP];
-      split_state<IO, D, 3>(wp, w);
-      const __amdgpu_buffer_rsrc_t dst = gl_span(dq + static_cast<size_t>(c0) * D, min(kC, T - c0) * D * static_cast<int>(sizeof(IO)));
-#pragma unroll
-      for (int ut = 0; ut < 4; ++ut) {
-        const int u = 16 * ut + r;
-        const gl_f4 xi = keep4(dec.from[u], state_times<IO, D, 3>(wp, L.z + u * LD, g));
-        gl_f4 xp = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int p = 0; p <= ut / 2; ++p) xp = M::mma_planes(kf[p], L.r + u * LDP, S::kPlane, p, g, xp);
-        if (row_o) {
-          const float in = over_g(dot4(M::template row4<D>(L.q + u * LD, wv, g), xi));
-          if (g == 0) L.part[wv][u] = in;
-        }
-        M::store4(xi + xp, dst, u * D + 16 * wv + 4 * g);
-      }
-      update_state<IO, D, 3>(w, dec.whole[0], L.v, kf, dec.to_e, g, r);
-      float in = 0.0f, row = 0.0f;
-      if (row_o) {
-        gl_barrier();
-#pragma unroll
-        for (int x = 0; x < NW; ++x) in += L.part[x][lane];
-#pragma unroll
-        for (int st = 0; st < 4; ++st) row += st <= lane >> 4 ? L.pairs[st][lane] : 0.0f;
-      }
-      store1(in, per_token(in_o, c0), lane);
-      store1(row, per_token(row_o, c0), lane);
-    }
-    if (row_o) {  // <G, W> at the segment's end
-      double x = 0.0;
-      if (g_end) {
-#pragma unroll
-        for (int b = 0; b < NW; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x += static_cast<double>(w[b][e]) * g_end[(16 * b + 4 * g + e) * D + 16 * wv + r];
+      for (int i = 0; i < N; ++i) {
+        ut[i] = block_row(first_block + i * 2 * NW);
+        st[i] = first_block + i * 2 * NW - ut[i] * (ut[i] + 1) / 2;
+        p[i] = row_products<IO, D>(L.q + (16 * ut[i] + r) * LD, L.k + (16 * st[i] + r) * LD, g);
+        rd[i] = row_products<IO, D>(L.z + (16 * ut[i] + r) * LD, L.v + (16 * st[i] + r) * LD, g);
       }
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
-      if (lane == 0) a.ws_end[static_cast<size_t>(item) * NW + wv] = x;
-    }
-  } else {
-    gl_f4 gt[NW], gn[NW];  // G twice: its rows 16 wv + r, its columns 16 wv + r
-    load_state<D, true>(gt, g_end, wv, g, r);
-    load_state<D, false>(gn, g_end, wv, g, r);
-    IO* dk = static_cast<IO*>(a.dk) + s.row0 * D;
-    IO* dv = static_cast<IO*>(a.dv) + s.row0 * D;
-    float* de_o = a.deta_tok ? a.deta_tok + s.row0 : nullptr;
-    begin(end - 1, end - 2);
-    no_store<11>();
-    zero_unused<IO, D, false>(L.p, wv, g, r);
-    zero_unused<IO, D, false>(L.r, wv, g, r);
-    for (int c = end - 1; c >= first; --c) {
-      const int c0 = c * kC, turn = (end - 1 - c) & 1;
-      const GlDecays& dec = L.dec[turn];
-      stage(c, c - 1, c - 2, turn);
-      // rows s of P^T and R^T (decayed, without e_s)
-      wave_blocks<NW>(wv, [&](auto n, int first_block) {
-        constexpr int N = n.value;
-        gl_f4 p[N], rd[N];
-        int ut[N], st[N];
+      for (int i = 0; i < N; ++i) {
+        const int ss = 16 * st[i] + r, u4 = 16 * ut[i] + 4 * g;
+        const float sh = dec.bh[ss], sl = dec.bl[ss], es = dec.e[ss];
+        const gl_f4 uh = at4(dec.bh, u4), ul = at4(dec.bl, u4);
+        float cs = 0.0f, dg = 0.0f;
+        gl_f4 rows;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          ut[i] = block_row(first_block + i * NW);
-          st[i] = first_block + i * NW - ut[i] * (ut[i] + 1) / 2;
-          p[i] = row_products<IO, D>(L.q + (16 * ut[i] + r) * LD, L.k + (16 * st[i] + r) * LD, g);
-          rd[i] = row_products<IO, D>(L.z + (16 * ut[i] + r) * LD, L.v + (16 * st[i] + r) * LD, g);
+        for (int j = 0; j < 4; ++j) {
+          const float f = gl_between(uh[j], ul[j], sh, sl);
+          const float m = p[i][j] * rd[i][j] * f, below = u4 + j > ss ? m : 0.0f;
+          p[i][j] = u4 + j >= ss ? p[i][j] * f : 0.0f;
+          rd[i][j] = u4 + j >= ss ? rd[i][j] * f : 0.0f;
+          cs += below;
+          dg += u4 + j == ss ? m : 0.0f;
+          rows[j] = below * es;
         }
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int ss = 16 * st[i] + r, u4 = 16 * ut[i] + 4 * g;
-          const float sh = dec.bh[ss], sl = dec.bl[ss];
-          const gl_f4 uh = at4(dec.bh, u4), ul = at4(dec.bl, u4);
-          float cs = 0.0f, dg = 0.0f;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float f = gl_between(uh[x], ul[x], sh, sl);
-            const float m = p[i][x] * rd[i][x] * f;
-            p[i][x] = u4 + x >= ss ? p[i][x] * f : 0.0f;
-            rd[i][x] = u4 + x >= ss ? rd[i][x] * f : 0.0f;
-            cs += u4 + x > ss ? m : 0.0f;
-            dg += u4 + x == ss ? m : 0.0f;
-          }
-          cs = over_g(cs);
-          if (g == 0) L.pairs[ut[i]][ss] = cs;
-          if (ut[i] == st[i]) {
-            dg = over_g(dg);
-            if (g == 0) L.diag[ss] = dg;
-          }
+        for (int j = 0; j < 4; ++j) rows[j] = over_r(rows[j]);
+        if (r == 0) *reinterpret_cast<gl_f4*>(&L.rows[st[i]][u4]) = rows;
+        cs = over_g(cs);
+        if (g == 0) L.pairs[ut[i]][ss] = cs;
+        if (ut[i] == st[i]) {
+          dg = over_g(dg);
+          if (g == 0) L.diag[ss] = dg;
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          M::put(L.p + (16 * st[i] + r) * LDP, S::kPlane, ut[i], g, p[i]);
-          M::put(L.r + (16 * st[i] + r) * LDP, S::kPlane, ut[i], g, rd[i]);
-        }
-      });
-      gl_barrier();
-      typename M::Op zf[2], qf[2];  // dZ and Q, k down the tokens u, the wave's features
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        zf[p] = M::template down<D>(L.z, LD, p, wv, g, r);
-        qf[p] = M::template down<D>(L.q, LD, p, wv, g, r);
       }
-      typename M::template Parts<3> tp[S::kNP];
-      typename M::template Parts<2> np[S::kNP];
-      split_state<IO, D, 3>(tp, gt);
-      split_state<IO, D, 2>(np, gn);
-      const int bytes = min(kC, T - c0) * D * static_cast<int>(sizeof(IO));
-      const __amdgpu_buffer_rsrc_t dstv = gl_span(dv + static_cast<size_t>(c0) * D, bytes);
-      const __amdgpu_buffer_rsrc_t dstk = gl_span(dk + static_cast<size_t>(c0) * D, bytes);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        M::put(L.p + (16 * st[i] + r) * LDP, S::kPlane, ut[i], g, p[i]);
+        M::put(L.r + (16 * st[i] + r) * LDP, S::kPlane, ut[i], g, rd[i]);
+      }
+    });
+    gl_barrier();
+    const __amdgpu_buffer_rsrc_t dst = gl_span(out + static_cast<size_t>(c0) * D, min(kC, T - c0) * D * static_cast<int>(sizeof(IO)));
+    // rows: the tile that the state multiplies; near, far: the tiles of the state's update;
+    // f: the chunk's factor; N: the state's parts
+    auto rest = [&](auto n, const typename S::Elem* rows, const typename S::Elem* near, const typename S::Elem* far,
+                    const typename S::Elem* f) {
+      constexpr int N = n.value;
+      typename M::Op b[2];  // k down the tokens u, the wave's features
+#pragma unroll
+      for (int p = 0; p < 2; ++p) b[p] = M::template down<D>(near, LD, p, wv, g, r);
+      typename M::template Parts<N> xp[S::kNP];
+      split_state<IO, D, N>(xp, x);
 #pragma unroll
       for (int st = 0; st < 4; ++st) {
         const int ss = 16 * st + r;
-        const float f = dec.to[ss], e = dec.e[ss];
-        const gl_f4 vi = keep4(f, state_times<IO, D, 3>(tp, L.k + ss * LD, g));
-        const gl_f4 ki = keep4(f, state_times<IO, D, 2>(np, L.v + ss * LD, g));
-        gl_f4 vp = {0.0f, 0.0f, 0.0f, 0.0f}, kp = vp;
+        const gl_f4 xi = keep4(dec.to[ss], state_times<IO, D, N>(xp, rows + ss * LD, g));
+        gl_f4 xc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int p = st / 2; p < 2; ++p) {
-          vp = M::mma_planes(zf[p], L.p + ss * LDP, S::kPlane, p, g, vp);
-          kp = M::mma_planes(qf[p], L.r + ss * LDP, S::kPlane, p, g, kp);
+        for (int p = st / 2; p < 2; ++p) xc = M::mma_planes(b[p], f + ss * LDP, S::kPlane, p, g, xc);
+        if constexpr (N == 3) {  // dv
+          const float o = over_g(dot4(M::template row4<D>(L.v + ss * LD, wv, g), xi));
+          if (g == 0) L.part[wv][ss] = o;
         }
-        const float out = over_g(dot4(M::template row4<D>(L.v + ss * LD, wv, g), vi));
-        if (g == 0) L.part[wv][ss] = out;
-        M::store4(e * (vi + vp), dstv, ss * D + 16 * wv + 4 * g);
-        M::store4(e * (ki + kp), dstk, ss * D + 16 * wv + 4 * g);
+        M::store4(dec.e[ss] * (xi + xc), dst, ss * D + 16 * wv + 4 * g);
       }
-      const float whole = dec.whole[0];
-      update_state<IO, D, 3>(gt, whole, L.q, zf, dec.from, g, r);
-      update_state<IO, D, 2>(gn, whole, L.z, qf, dec.from, g, r);
-      gl_barrier();
-      float out = 0.0f, col = 0.0f;
-#pragma unroll
-      for (int x = 0; x < NW; ++x) out += L.part[x][lane];
-#pragma unroll
-      for (int ut = 0; ut < 4; ++ut) col += ut >= lane >> 4 ? L.pairs[ut][lane] : 0.0f;
-      const float e = dec.e[lane];
-      store1(c0 + lane < s.len ? a.eta * (col + L.diag[lane] + out) : 0.0f, per_token(de_o, c0), lane);
-      store1(e * col, per_token(col_o, c0), lane);
-      store1(e * out, per_token(out_o, c0), lane);
-    }
-    if (seg == 0) store_state_transposed<D>(gt, a.dw0 + static_cast<size_t>(chain) * D * D, wv, g, r);
+      update_state<IO, D, N>(x, dec.whole[0], far, b, dec.from, g, r);
+    };
+    if (dk_group) rest(std::integral_constant<int, 2>(), L.v, L.q, L.z, L.r);
+    else rest(std::integral_constant<int, 3>(), L.k, L.z, L.q, L.p);
   }
+  if (first < end) {
+    gl_barrier();
+    flush(first, L.dec[(end - 1 - first) & 1].e);
+  }
+  if (seg == 0 && !dk_group) store_state_transposed<D>(x, a.dw0 + static_cast<size_t>(chain) * D * D, wv, g, r);
 }
 
 // dlog_gate from the per-token sums (see above): one wave per chunk, lane = token.  Each wave
@@ -898,17 +983,26 @@ __global__ __launch_bounds__(256) void gl_dgate_kernel(GatedArgs a, int nend) {
 
 // ---------------------------------------------------------------- host
 
-// Chunks per segment.
-int chunks_per_segment(long long chains, int nchunks, int want) {
-  const long long segs = (want + chains - 1) / chains;  // workgroups wanted
-  const long long n = segs < 1 ? 1 : segs;
-  const long long spc = (nchunks + n - 1) / n;
-  return spc < 1 ? 1 : static_cast<int>(spc);
-}
+// Chunks per segment: the number of segments that takes the fewest rounds of chunks, where `slots`
+// workgroups run at once and each spends about kStart chunks' time before its first.
 void plan(GatedArgs* a, bool bwd) {
-  const int nchunks = (a->T + kC - 1) / kC;
-  a->spc = chunks_per_segment(static_cast<long long>(a->B) * a->H, nchunks, getenv("GL_WANT") ? atoi(getenv("GL_WANT")) : 512);
-  a->nseg = nchunks > 0 ? (nchunks + a->spc - 1) / a->spc : 1;
+  constexpr int kStart = 2;
+  const int slots = getenv("GL_WANT") ? atoi(getenv("GL_WANT")) : bwd ? 512 : 768;
+  const long long nchunks = (a->T + kC - 1) / kC, chains = static_cast<long long>(a->B) * a->H;
+  long long best = -1;
+  a->spc = 1;
+  a->nseg = 1;
+  for (long long n = 1; n <= nchunks && n <= 512; ++n) {
+    const long long spc = (nchunks + n - 1) / n, nseg = (nchunks + spc - 1) / spc;
+    if (nseg < n) continue;  // as many segments come from a smaller n
+    const long long cost = (chains * nseg + slots - 1) / slots * (spc + kStart);
+    if (best < 0 || cost < best) {
+      best = cost;
+      a->spc = static_cast<int>(spc);
+      a->nseg = static_cast<int>(nseg);
+    }
+    if (chains * nseg > 4 * slots) break;
+  }
 }
 
 template <typename F>
@@ -945,12 +1039,16 @@ hipError_t fwd(const GatedArgs& a, hipStream_t s) {
 
 template <typename IO, int D>
 hipError_t bwd(const GatedArgs& a, hipStream_t s) {
-  const auto fn = gl_bwd_kernel<IO, D>;
-  constexpr int bytes = sizeof(BwdLds<IO, D>);
-  hipError_t e = allow_lds(fn, bytes);
+  const auto dq = gl_dq_kernel<IO, D>;
+  const auto dkv = gl_dkv_kernel<IO, D>;
+  constexpr int dq_bytes = sizeof(DqLds<IO, D>), dkv_bytes = sizeof(DkvLds<IO, D>);
+  hipError_t e = allow_lds(dq, dq_bytes);
+  if (e == hipSuccess) e = allow_lds(dkv, dkv_bytes);
   if (e == hipSuccess) e = segment_states<IO, D>(a, 2, s);
   if (e != hipSuccess) return e;
-  fn<<<dim3(16 * ((a.B * a.H * a.nseg + 7) / 8)), dim3(4 * D), bytes, s>>>(a);
+  const int groups = a.B * a.H * a.nseg;
+  if (a.T > 0) dq<<<dim3(groups), dim3(4 * D), dq_bytes, s>>>(a);
+  dkv<<<dim3(groups), dim3(8 * D), dkv_bytes, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess || !a.dgate || a.T == 0) return e;
   const long long items = static_cast<long long>(a.B) * a.H * ((a.T + kC - 1) / kC);
