@@ -7,8 +7,8 @@
 // The d x d state stays in registers, 16 columns a wave, in the MFMA C layout.
 //
 // Every product is a sum of 16 x 16 tiles C = A B.  Lane (g, r) of a wave holds row r of A and
-// column r of B at k = 4 g + e and k = 16 + 4 g + e (e = 0..3) of each block of 32 k, and rows
-// 4 g + e of column r of C.  So two C tiles are an operand whose k runs along their rows, with no
+// column r of B at eight k of each block of 32, the same ones for both, and rows 4 g + e (e =
+// 0..3) of column r of C.  So two C tiles are an operand whose k runs along their rows, with no
 // exchange between lanes: the state feeds the next chunk's products as it is.
 //
 //   float32 I/O:  v_mfma_f32_16x16x4_f32.
@@ -66,8 +66,7 @@ template <typename IO> struct Math;
 template <>
 struct Math<float> {
   typedef float Elem;
-  static constexpr int kPad = 4;       // row pitch = columns + kPad: 16-byte rows, spread over the banks
-  static constexpr int kPlanes = 1;    // matrices that hold one product's factor
+  template <int D> static constexpr int pitch() { return D + 4; }
   struct Op { gl_f4 a, b; };
   template <int N> struct Parts { Op x; };
   template <bool Half> static __device__ __forceinline__ Op along(const float* row, int p, int g) {
@@ -98,12 +97,25 @@ struct Math<float> {
     *a = x.a;
     *b = x.b;
   }
-  // the factor's columns 16 cb + 4 g .. + 3 of one row
-  static __device__ __forceinline__ void put(float* row, int, int cb, int g, const gl_f4& x) {
+  // A factor of token pairs: columns 16 cb + 4 g .. + 3 of a row, and its product over block cb.
+  // `Block`: the other operand over 16 tokens.
+  typedef gl_f4 Block;
+  static constexpr int kBlock = 16, kBlockPad = 4;  // elements of a block in a row, of a row's padding
+  static __device__ __forceinline__ void put(float* row, int cb, int g, const gl_f4& x) {
     *reinterpret_cast<gl_f4*>(row + 16 * cb + 4 * g) = x;
   }
-  static __device__ __forceinline__ gl_f4 mma_planes(const Op& a, const float* row, int, int p, int g, gl_f4 c) {
-    return mma<false>(a, along<false>(row, p, g), c);
+  static __device__ __forceinline__ Block block(const Op& x, int half) { return half ? x.b : x.a; }
+  static __device__ __forceinline__ gl_f4 mma_factor(const Block& a, const float* row, int cb, int g, gl_f4 c) {
+    const gl_f4 b = at4(row, 16 * cb + 4 * g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+  // feature of row 4 g of tile b of a state
+  template <int D> static __device__ __forceinline__ int state_row(int b, int g) { return 16 * b + 4 * g; }
+  // the same features of a token tile as rows of an operand, k down the tokens
+  template <int D> static __device__ __forceinline__ Op down_state(const float* m, int ld, int p, int b, int g, int r) {
+    return down<D>(m, ld, p, b, g, r);
   }
   template <int D> static __device__ __forceinline__ gl_f4 row4(const float* row, int cb, int g) { return at4(row, 16 * cb + 4 * g); }
   typedef gl_f4 Four;  // four features of a token, from element `elem` of the source
@@ -116,33 +128,49 @@ struct Math<float> {
   }
   template <int D> static __device__ __forceinline__ void put_vec(float* m, int vec, const gl_u4& x) {
     const int at = vec * 4;
-    *reinterpret_cast<gl_u4*>(m + (at / D) * (D + kPad) + at % D) = x;
+    *reinterpret_cast<gl_u4*>(m + (at / D) * pitch<D>() + at % D) = x;
   }
 };
 
 template <>
 struct Math<bf16> {
   typedef bf16 Elem;
-  static constexpr int kPad = 8;
-  static constexpr int kPlanes = 2;  // hi and lo
+  // Rows of 160 bytes (96 at d = 32): with 64 banks of 4 bytes, 16-byte reads of 16 rows and
+  // transposing reads both run without conflicts (4 and 2 cycles a wave, measured).  Rows of 144
+  // bytes: 8 and 4; two 8-byte reads of a lane, which the compiler joins, take 16.
+  template <int D> static constexpr int pitch() { return D == 16 ? 24 : D + 16; }
   typedef gl_b8 Op;
   template <int N> struct Parts { Op x[N]; };
-  // eight k of a block: columns 32 p + 4 g .. + 3 and 32 p + 16 + 4 g .. + 3
+  // eight k of a block: columns 32 p + 8 g .. + 7 (d = 16: 4 g .. + 3)
   template <bool Half> static __device__ __forceinline__ Op along(const bf16* row, int p, int g) {
-    const gl_b4 x = *reinterpret_cast<const gl_b4*>(row + 32 * p + 4 * g);
-    const gl_b4 y = Half ? x : *reinterpret_cast<const gl_b4*>(row + 32 * p + 4 * g + (Half ? 0 : 16));
-    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    if constexpr (Half) {
+      const gl_b4 x = *reinterpret_cast<const gl_b4*>(row + 4 * g);
+      return __builtin_shufflevector(x, x, 0, 1, 2, 3, 0, 1, 2, 3);
+    }
+    return *reinterpret_cast<const gl_b8*>(row + 32 * p + 8 * g);
   }
   // Transposing LDS read: the 16 lanes of a group give the addresses of four rows' 16 columns
   // (lane 4 i + j: row i, columns 4 j .. + 3) and receive one column of four rows each.
-  static __device__ __forceinline__ gl_s4 down16(const bf16* m, int ld, int k0, int cb, int g, int r) {
-    const bf16* q = m + (k0 + 4 * g + (r >> 2)) * ld + 16 * cb + 4 * (r & 3);
+  static __device__ __forceinline__ gl_s4 down16(const bf16* m, int ld, int k0, int column, int g, int r) {
+    const bf16* q = m + (k0 + 4 * g + (r >> 2)) * ld + column;
     typedef __attribute__((address_space(3))) gl_s4 lds_s4;
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)q);
   }
+  // k = 32 p + 4 g + e and 32 p + 16 + 4 g + e down the rows, columns 16 cb + r
   template <int D> static __device__ __forceinline__ Op down(const bf16* m, int ld, int p, int cb, int g, int r) {
-    const gl_s4 a = down16(m, ld, 32 * p, cb, g, r), b = down16(m, ld, 32 * p + 16, cb, g, r);
+    return down_at(m, ld, p, 16 * cb + 4 * (r & 3), g, r);
+  }
+  static __device__ __forceinline__ Op down_at(const bf16* m, int ld, int p, int column, int g, int r) {
+    const gl_s4 a = down16(m, ld, 32 * p, column, g, r), b = down16(m, ld, 32 * p + 16, column, g, r);
     return __builtin_bit_cast(gl_b8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  // A state's rows follow `along`: rows 4 g + e of tiles 2 p and 2 p + 1 are features 32 p + 8 g + e
+  // and 32 p + 8 g + 4 + e.
+  template <int D> static __device__ __forceinline__ int state_row(int b, int g) {
+    return D == 16 ? 4 * g : 32 * (b >> 1) + 8 * g + 4 * (b & 1);
+  }
+  template <int D> static __device__ __forceinline__ Op down_state(const bf16* m, int ld, int p, int b, int g, int r) {
+    return down_at(m, ld, p, state_row<D>(b, r & 3), g, r);
   }
   template <bool Half> static __device__ __forceinline__ gl_f4 mma(const Op& a, const Op& b, gl_f4 c) {
     if constexpr (Half) {
@@ -186,19 +214,26 @@ struct Math<bf16> {
     *a = gl_f4{gl_lo(w[0]), gl_hi(w[0]), gl_lo(w[1]), gl_hi(w[1])};
     *b = gl_f4{gl_lo(w[2]), gl_hi(w[2]), gl_lo(w[3]), gl_hi(w[3])};
   }
-  static __device__ __forceinline__ void put(bf16* row, int plane, int cb, int g, const gl_f4& x) {
+  // A factor of token pairs keeps its two parts side by side, four columns of hi and the same of
+  // lo, so that a lane writes and reads 16 bytes: one product over 32 k is 16 tokens' hi and lo
+  // against the other operand twice.  Rows of 96, 160, 224 and 288 bytes (no conflicts, as above).
+  typedef gl_b8 Block;
+  static constexpr int kBlock = 32, kBlockPad = 16;
+  static __device__ __forceinline__ void put(bf16* row, int cb, int g, const gl_f4& x) {
     const uint32_t a = gl_pack(x[0], x[1]), b = gl_pack(x[2], x[3]);
-    const int at = 16 * cb + 4 * g;
-    *reinterpret_cast<gl_u2*>(row + at) = gl_u2{a, b};
-    *reinterpret_cast<gl_u2*>(row + plane + at) =
-        gl_u2{gl_pack(x[0] - gl_lo(a), x[1] - gl_hi(a)), gl_pack(x[2] - gl_lo(b), x[3] - gl_hi(b))};
+    *reinterpret_cast<gl_u4*>(row + 32 * cb + 8 * g) =
+        gl_u4{a, b, gl_pack(x[0] - gl_lo(a), x[1] - gl_hi(a)), gl_pack(x[2] - gl_lo(b), x[3] - gl_hi(b))};
   }
-  static __device__ __forceinline__ gl_f4 mma_planes(const Op& a, const bf16* row, int plane, int p, int g, gl_f4 c) {
-    c = mma<false>(a, along<false>(row + plane, p, g), c);
-    return mma<false>(a, along<false>(row, p, g), c);
+  static __device__ __forceinline__ Block block(const Op& x, int half) {
+    return half ? __builtin_shufflevector(x, x, 4, 5, 6, 7, 4, 5, 6, 7) : __builtin_shufflevector(x, x, 0, 1, 2, 3, 0, 1, 2, 3);
   }
+  static __device__ __forceinline__ gl_f4 mma_factor(const Block& a, const bf16* row, int cb, int g, gl_f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, *reinterpret_cast<const gl_b8*>(row + 32 * cb + 8 * g), c, 0, 0, 0);
+  }
+  // columns 16 cb + 4 g .. + 3 of a row, from a 16-byte read that two g share
   template <int D> static __device__ __forceinline__ gl_f4 row4(const bf16* row, int cb, int g) {
-    return widen4(*reinterpret_cast<const gl_u2*>(row + 16 * cb + 4 * g));
+    const gl_u4 w = *reinterpret_cast<const gl_u4*>(row + 16 * cb + 8 * (g >> 1));
+    return widen4(g & 1 ? gl_u2{w[2], w[3]} : gl_u2{w[0], w[1]});
   }
   typedef gl_u2 Four;
   static __device__ __forceinline__ Four load4(__amdgpu_buffer_rsrc_t src, int elem) {
@@ -211,20 +246,42 @@ struct Math<bf16> {
   }
   template <int D> static __device__ __forceinline__ void put_vec(bf16* m, int vec, const gl_u4& x) {
     const int at = vec * 8;
-    *reinterpret_cast<gl_u4*>(m + (at / D) * (D + kPad) + at % D) = x;
+    *reinterpret_cast<gl_u4*>(m + (at / D) * pitch<D>() + at % D) = x;
   }
 };
+// Blocks (ut, st), st <= ut, of 16 tokens each in a chunk's triangle of token pairs, in order.
+constexpr int kBlocks = 10;
+__device__ __forceinline__ int block_row(int t) { return t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0; }
+// The blocks wv, wv + NW, ... of a wave, two at a time where there are two, so that one's LDS reads
+// and products run under the other's: f(n, first), n blocks first, first + NW.
+template <int NW, typename F>
+__device__ __forceinline__ void wave_blocks(int wv, F f) {
+  constexpr int kAll = kBlocks / NW;  // of every wave
+#pragma unroll
+  for (int i = 0; i + 2 <= kAll; i += 2) f(std::integral_constant<int, 2>(), wv + i * NW);
+  if constexpr (kAll % 2) f(std::integral_constant<int, 1>(), wv + (kAll - 1) * NW);
+  if constexpr (kBlocks % NW) {
+    if (wv < kBlocks % NW) f(std::integral_constant<int, 1>(), wv + kAll * NW);
+  }
+}
+
 template <typename IO, int D>
 struct Shape {
   typedef typename Math<IO>::Elem Elem;
   static constexpr int kNW = D / 16;                           // waves
   static constexpr int kNP = D / 32 > 0 ? D / 32 : 1;          // blocks of 32 features
   static constexpr bool kHalf = D == 16;
-  static constexpr int kLd = D + Math<IO>::kPad;               // row pitch of a token tile
+  static constexpr int kLd = Math<IO>::template pitch<D>();    // row pitch of a token tile
   static constexpr int kTile = kC * kLd;
-  static constexpr int kLdP = kC + Math<IO>::kPad;             // row pitch of a factor of token pairs
-  static constexpr int kPlane = kC * kLdP;
+  static constexpr int kFactor = 16 * (kBlocks * Math<IO>::kBlock + 4 * Math<IO>::kBlockPad);
 };
+
+// Row 16 t + r of a triangular factor: t + 1 blocks of 16 columns.
+template <typename IO>
+__device__ __forceinline__ typename Math<IO>::Elem* factor_row(typename Math<IO>::Elem* m, int t, int r) {
+  constexpr int B = Math<IO>::kBlock, P = Math<IO>::kBlockPad;
+  return m + 16 * (B * (t * (t + 1) / 2) + P * t) + r * (B * (t + 1) + P);
+}
 
 // Loads.  A tile's registers are filled by buffer loads whose range ends at the last valid token
 // (0 bytes for a chunk outside the segment), so every wave issues the same ones on every path.
@@ -255,22 +312,6 @@ template <int N>
 __device__ __forceinline__ void no_store() {
 #pragma unroll
   for (int i = 0; i < N; ++i) store1(0.0f, gl_span(nullptr, 0), 0);
-}
-
-// Blocks (ut, st), st <= ut, of 16 tokens each in a chunk's triangle of token pairs, in order.
-constexpr int kBlocks = 10;
-__device__ __forceinline__ int block_row(int t) { return t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0; }
-// The blocks wv, wv + NW, ... of a wave, two at a time where there are two, so that one's LDS reads
-// and products run under the other's: f(n, first), n blocks first, first + NW.
-template <int NW, typename F>
-__device__ __forceinline__ void wave_blocks(int wv, F f) {
-  constexpr int kAll = kBlocks / NW;  // of every wave
-#pragma unroll
-  for (int i = 0; i + 2 <= kAll; i += 2) f(std::integral_constant<int, 2>(), wv + i * NW);
-  if constexpr (kAll % 2) f(std::integral_constant<int, 1>(), wv + (kAll - 1) * NW);
-  if constexpr (kBlocks % NW) {
-    if (wv < kBlocks % NW) f(std::integral_constant<int, 1>(), wv + kAll * NW);
-  }
 }
 
 // One sequence's view of the arguments.
@@ -310,24 +351,26 @@ __device__ __forceinline__ const float* initial_state(const GatedArgs& a, int ch
 }
 
 
-// A state in registers.  Tile b of wave wv holds X[16 b + 4 g + e][16 wv + r] of the matrix X that
-// `rows` says is W (false: W^T, so that W's rows lie along the registers).
-template <int D, bool kTransposed>
+// A state in registers: row 4 g + e of tile b and column r of wave wv are the elements (f + e,
+// 16 wv + r), f = state_row(b, g), of W, or of W^T (kTransposed).
+template <typename IO, int D, bool kTransposed>
 __device__ __forceinline__ void load_state(gl_f4* x, const float* w, int wv, int g, int r) {
 #pragma unroll
   for (int b = 0; b < D / 16; ++b) {
+    const int f = Math<IO>::template state_row<D>(b, g);
     if constexpr (kTransposed) {
-      x[b] = w ? at4(w, (16 * wv + r) * D + 16 * b + 4 * g) : gl_f4{0.0f, 0.0f, 0.0f, 0.0f};
+      x[b] = w ? at4(w, (16 * wv + r) * D + f) : gl_f4{0.0f, 0.0f, 0.0f, 0.0f};
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[b][e] = w ? w[(16 * b + 4 * g + e) * D + 16 * wv + r] : 0.0f;
+      for (int e = 0; e < 4; ++e) x[b][e] = w ? w[(f + e) * D + 16 * wv + r] : 0.0f;
     }
   }
 }
-template <int D>
+template <typename IO, int D>
 __device__ __forceinline__ void store_state_transposed(const gl_f4* x, float* w, int wv, int g, int r) {
 #pragma unroll
-  for (int b = 0; b < D / 16; ++b) *reinterpret_cast<gl_f4*>(w + (16 * wv + r) * D + 16 * b + 4 * g) = x[b];
+  for (int b = 0; b < D / 16; ++b)
+    *reinterpret_cast<gl_f4*>(w + (16 * wv + r) * D + Math<IO>::template state_row<D>(b, g)) = x[b];
 }
 
 // x <- whole x + sum over the chunk's tokens s of a_s c_s b_s^T, a the rows of the tile A, b the
@@ -353,7 +396,7 @@ __device__ __forceinline__ void update_state(gl_f4* x, float whole, const typena
     const typename M::template Parts<N> f = M::template split<N>(lo, hi);
 #pragma unroll
     for (int ab = 0; ab < D / 16; ++ab)
-      x[ab] = M::template mma_cols<N, false>(M::template down<D>(A, Shape<IO, D>::kLd, p, ab, g, r), f, x[ab]);
+      x[ab] = M::template mma_cols<N, false>(M::template down_state<D>(A, Shape<IO, D>::kLd, p, ab, g, r), f, x[ab]);
   }
 }
 // the state as an operand: parts over blocks of 32 rows
@@ -382,17 +425,6 @@ __device__ __forceinline__ gl_f4 row_products(const typename Math<IO>::Elem* a, 
   for (int p = 0; p < S::kNP; ++p)
     c = Math<IO>::template mma<S::kHalf>(Math<IO>::template along<S::kHalf>(a, p, g), Math<IO>::template along<S::kHalf>(b, p, g), c);
   return c;
-}
-
-// Blocks of a factor that a product over 32 tokens reads and that no pair (u, s), s <= u, reaches:
-// (rows u, columns s) = (0, 1) and (2, 3), transposed (1, 0) and (3, 2).  They stay 0.
-template <typename IO, int D, bool kRowsAreU>
-__device__ __forceinline__ void zero_unused(typename Math<IO>::Elem* m, int wv, int g, int r) {
-  typedef Shape<IO, D> S;
-  if (wv != 0) return;
-#pragma unroll
-  for (int i = 0; i < 4; i += 2)
-    Math<IO>::put(m + (16 * (kRowsAreU ? i : i + 1) + r) * S::kLdP, S::kPlane, kRowsAreU ? i + 1 : i, g, gl_f4{0.0f, 0.0f, 0.0f, 0.0f});
 }
 
 // ---------------------------------------------------------------- segments
@@ -462,7 +494,7 @@ __global__ __launch_bounds__(4 * D) void gl_sums_kernel(GatedArgs a) {
     update_state<IO, D, 3>(x, whole, L.a, b, side == 0 ? dec.to_e : dec.from, g, r);
   }
   float* out = (side == 0 ? a.seg_w : a.seg_g) + static_cast<size_t>(blockIdx.x) * D * D;
-  store_state_transposed<D>(x, out, wv, g, r);
+  store_state_transposed<IO, D>(x, out, wv, g, r);
   if (tid == 0) a.seg_decay[static_cast<size_t>(side) * a.B * a.H * a.nseg + blockIdx.x] = all;
 }
 
@@ -509,7 +541,7 @@ __device__ __forceinline__ const float* segment_state(const GatedArgs& a, int si
 template <typename IO, int D>
 struct FwdLds {
   typename Math<IO>::Elem q[Shape<IO, D>::kTile], k[Shape<IO, D>::kTile], v[Shape<IO, D>::kTile];
-  typename Math<IO>::Elem p[Math<IO>::kPlanes * Shape<IO, D>::kPlane];
+  typename Math<IO>::Elem p[Shape<IO, D>::kFactor];
   GlDecays dec[2];  // of this chunk and the next
 };
 
@@ -517,7 +549,7 @@ template <typename IO, int D>
 __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
   typedef Math<IO> M;
   typedef Shape<IO, D> S;
-  constexpr int NW = S::kNW, LD = S::kLd, LDP = S::kLdP;
+  constexpr int NW = S::kNW, LD = S::kLd;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
   FwdLds<IO, D>& L = *reinterpret_cast<FwdLds<IO, D>*>(lds_raw);
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
@@ -531,7 +563,7 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
   const int nchunks = (T + kC - 1) / kC, first = seg * a.spc, end = min(nchunks, first + a.spc);
 
   gl_f4 w[NW];  // W^T: W's rows 16 wv + r
-  load_state<D, true>(w, segment_state<D>(a, 0, chain, seg), wv, g, r);
+  load_state<IO, D, true>(w, segment_state<D>(a, 0, chain, seg), wv, g, r);
   // what a chunk's step needs in registers: its tiles, and the gates of the chunk after it
   struct Set {
     Tile<IO, D> q, k, v;
@@ -553,7 +585,6 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
     no_store<4>();
     if (decayer) gr.decays(s, a.eta, static_cast<long long>(first) * kC, &L.dec[0], lane);
   }
-  zero_unused<IO, D, true>(L.p, wv, g, r);
   for (int c = first; c < end; ++c) {
     const int c0 = c * kC;
     const GlDecays& dec = L.dec[(c - first) & 1];
@@ -586,7 +617,7 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
         for (int x = 0; x < 4; ++x) p[i][x] = s4 + x <= u ? p[i][x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i) M::put(L.p + (16 * ut[i] + r) * LDP, S::kPlane, st[i], g, p[i]);
+      for (int i = 0; i < N; ++i) M::put(factor_row<IO>(L.p, ut[i], r), st[i], g, p[i]);
     });
     gl_barrier();
 
@@ -602,12 +633,12 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
       const gl_f4 zi = state_times<IO, D, 2>(wp, L.q + u * LD, g);
       gl_f4 zp = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int p = 0; p <= ut / 2; ++p) zp = M::mma_planes(vf[p], L.p + u * LDP, S::kPlane, p, g, zp);
+      for (int st = 0; st <= ut; ++st) zp = M::mma_factor(M::block(vf[st / 2], st % 2), factor_row<IO>(L.p, ut, r), st, g, zp);
       M::store4(zp + keep4(dec.from[u], zi), dst, u * D + 16 * wv + 4 * g);
     }
     update_state<IO, D, 3>(w, dec.whole[0], L.k, vf, dec.to_e, g, r);
   }
-  if (a.w_out && seg == a.nseg - 1) store_state_transposed<D>(w, a.w_out + static_cast<size_t>(chain) * D * D, wv, g, r);
+  if (a.w_out && seg == a.nseg - 1) store_state_transposed<IO, D>(w, a.w_out + static_cast<size_t>(chain) * D * D, wv, g, r);
 }
 
 // ---------------------------------------------------------------- backward
@@ -633,7 +664,7 @@ template <typename IO, int D>
 struct DqLds {
   typedef Shape<IO, D> S;
   typename S::Elem k[S::kTile], v[S::kTile], z[S::kTile];
-  typename S::Elem r[Math<IO>::kPlanes * S::kPlane];
+  typename S::Elem r[S::kFactor];
   float part[S::kNW][kC];  // in_u, the waves' shares
   GlDecays dec[2];         // of this chunk and the next
 };
@@ -642,7 +673,7 @@ template <typename IO, int D>
 __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
   typedef Math<IO> M;
   typedef Shape<IO, D> S;
-  constexpr int NW = S::kNW, LD = S::kLd, LDP = S::kLdP;
+  constexpr int NW = S::kNW, LD = S::kLd;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
   DqLds<IO, D>& L = *reinterpret_cast<DqLds<IO, D>*>(lds_raw);
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
@@ -688,8 +719,7 @@ __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
     no_store<5>();
     if (decayer) gr.decays(s, a.eta, static_cast<long long>(first) * kC, &L.dec[0], lane);
   }
-  load_state<D, false>(w, segment_state<D>(a, 0, chain, seg), wv, g, r);
-  zero_unused<IO, D, true>(L.r, wv, g, r);
+  load_state<IO, D, false>(w, segment_state<D>(a, 0, chain, seg), wv, g, r);
   for (int c = first; c < end; ++c) {
     const int c0 = c * kC, turn = (c - first) & 1;
     const GlDecays& dec = L.dec[turn];
@@ -726,7 +756,7 @@ __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
         for (int x = 0; x < 4; ++x) rd[i][x] = s4 + x <= u ? rd[i][x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i) M::put(L.r + (16 * ut[i] + r) * LDP, S::kPlane, st[i], g, rd[i]);
+      for (int i = 0; i < N; ++i) M::put(factor_row<IO>(L.r, ut[i], r), st[i], g, rd[i]);
     });
     gl_barrier();
     typename M::Op kf[2];
@@ -741,7 +771,7 @@ __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
       const gl_f4 xi = keep4(dec.from[u], state_times<IO, D, 3>(wp, L.z + u * LD, g));
       gl_f4 xp = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int p = 0; p <= ut / 2; ++p) xp = M::mma_planes(kf[p], L.r + u * LDP, S::kPlane, p, g, xp);
+      for (int st = 0; st <= ut; ++st) xp = M::mma_factor(M::block(kf[st / 2], st % 2), factor_row<IO>(L.r, ut, r), st, g, xp);
       const float in = over_g(dot4(M::widen4(qu[ut]), xi));
       if (g == 0) L.part[wv][u] = in;
       M::store4(xi + xp, dst, u * D + 16 * wv + 4 * g);
@@ -752,7 +782,7 @@ __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
   flush(end - 1);
   if (in_o) {  // <G, W> at the segment's end
     gl_f4 ge[NW];
-    load_state<D, false>(ge, segment_state<D>(a, 1, chain, seg), wv, g, r);
+    load_state<IO, D, false>(ge, segment_state<D>(a, 1, chain, seg), wv, g, r);
     double x = 0.0;
 #pragma unroll
     for (int b = 0; b < NW; ++b)
@@ -769,7 +799,7 @@ template <typename IO, int D>
 struct DkvLds {
   typedef Shape<IO, D> S;
   typename S::Elem q[S::kTile], k[S::kTile], v[S::kTile], z[S::kTile];
-  typename S::Elem p[Math<IO>::kPlanes * S::kPlane], r[Math<IO>::kPlanes * S::kPlane];
+  typename S::Elem p[S::kFactor], r[S::kFactor];  // P^T and R^T, the tiles of rows in reverse order
   float part[S::kNW][kC];  // v_s . G k_s to the chunk's end, the waves' shares
   float pairs[4][kC];      // col_s / e_s, the blocks' shares
   float rows[4][kC];       // row_u, the blocks' shares
@@ -781,7 +811,7 @@ template <typename IO, int D>
 __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
   typedef Math<IO> M;
   typedef Shape<IO, D> S;
-  constexpr int NW = S::kNW, LD = S::kLd, LDP = S::kLdP;
+  constexpr int NW = S::kNW, LD = S::kLd;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
   DkvLds<IO, D>& L = *reinterpret_cast<DkvLds<IO, D>*>(lds_raw);
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
@@ -806,7 +836,8 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
     Tile<IO, D, 8 * D> q, k, v, z;
     GateRate gr;
   } y;
-  auto fetch = [&](int c) {
+  auto fetch = [&](int c, int tid) {
+    const int lane = tid & 63;
     const long long c0 = static_cast<long long>(c) * kC;
     y.gr.load(s, c0 - kC, lane);
     const int valid = c >= first ? s.len - static_cast<int>(c0) : 0;
@@ -817,7 +848,7 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
   };
   const bool decayer = wave == 2 * NW - 1;  // the wave that forms the next chunk's decays
   // sums of a chunk whose shares are in LDS, stored by wave 0 (c >= end: nothing)
-  auto flush = [&](int c, const float* es) {
+  auto flush = [&](int c, const float* es, int lane) {
     const int c0 = c * kC, bytes = wave == 0 && c < end ? min(kC, T - c0) * 4 : 0;
     float o = 0.0f, col = 0.0f, row = 0.0f;
 #pragma unroll
@@ -839,26 +870,30 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
   if (first < end) {
     GateRate gr;
     gr.load(s, static_cast<long long>(end - 1) * kC, lane);
-    fetch(end - 1);
+    fetch(end - 1, tid);
     no_store<8>();
     if (decayer) gr.decays(s, a.eta, static_cast<long long>(end - 1) * kC, &L.dec[0], lane);
   }
-  if (dk_group) load_state<D, false>(x, segment_state<D>(a, 1, chain, seg), wv, g, r);
-  else load_state<D, true>(x, segment_state<D>(a, 1, chain, seg), wv, g, r);
-  zero_unused<IO, D, false>(L.p, wave, g, r);
-  zero_unused<IO, D, false>(L.r, wave, g, r);
+  if (dk_group) load_state<IO, D, false>(x, segment_state<D>(a, 1, chain, seg), wv, g, r);
+  else load_state<IO, D, true>(x, segment_state<D>(a, 1, chain, seg), wv, g, r);
   for (int c = end - 1; c >= first; --c) {
+    // The lane's addresses are formed anew for every chunk: kept across the loop they would not
+    // fit in the 128 registers that let two workgroups share a CU (and a spilled one's reload
+    // waits for the tiles on their way).
+    int here = threadIdx.x;
+    __asm__ __volatile__("" : "+v"(here));
+    const int tid = here, lane = tid & 63, g = lane >> 4, r = lane & 15;
     const int c0 = c * kC, turn = (end - 1 - c) & 1;
     const GlDecays& dec = L.dec[turn];
     gl_barrier();  // the previous chunk's tiles have been read, its sums are whole
-    flush(c + 1, L.dec[turn ^ 1].e);
+    flush(c + 1, L.dec[turn ^ 1].e, lane);
     y.q.put(L.q, tid);
     y.k.put(L.k, tid);
     y.v.put(L.v, tid);
     y.z.put(L.z, tid);
     const GateRate gr = y.gr;
     gl_barrier();
-    fetch(c - 1);
+    fetch(c - 1, tid);
     if (decayer && c > first) gr.decays(s, a.eta, static_cast<long long>(c - 1) * kC, &L.dec[turn ^ 1], lane);
     // rows s of P^T and R^T (decayed, without e_s)
     wave_blocks<2 * NW>(wave, [&](auto n, int first_block) {
@@ -901,8 +936,8 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        M::put(L.p + (16 * st[i] + r) * LDP, S::kPlane, ut[i], g, p[i]);
-        M::put(L.r + (16 * st[i] + r) * LDP, S::kPlane, ut[i], g, rd[i]);
+        M::put(factor_row<IO>(L.p, 3 - st[i], r), ut[i] - st[i], g, p[i]);
+        M::put(factor_row<IO>(L.r, 3 - st[i], r), ut[i] - st[i], g, rd[i]);
       }
     });
     gl_barrier();
@@ -910,7 +945,7 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
     // rows: the tile that the state multiplies; near, far: the tiles of the state's update;
     // f: the chunk's factor; N: the state's parts
     auto rest = [&](auto n, const typename S::Elem* rows, const typename S::Elem* near, const typename S::Elem* far,
-                    const typename S::Elem* f) {
+                    typename S::Elem* f) {
       constexpr int N = n.value;
       typename M::Op b[2];  // k down the tokens u, the wave's features
 #pragma unroll
@@ -923,7 +958,7 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
         const gl_f4 xi = keep4(dec.to[ss], state_times<IO, D, N>(xp, rows + ss * LD, g));
         gl_f4 xc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int p = st / 2; p < 2; ++p) xc = M::mma_planes(b[p], f + ss * LDP, S::kPlane, p, g, xc);
+        for (int ut = st; ut < 4; ++ut) xc = M::mma_factor(M::block(b[ut / 2], ut % 2), factor_row<IO>(f, 3 - st, r), ut - st, g, xc);
         if constexpr (N == 3) {  // dv
           const float o = over_g(dot4(M::template row4<D>(L.v + ss * LD, wv, g), xi));
           if (g == 0) L.part[wv][ss] = o;
@@ -937,9 +972,9 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
   }
   if (first < end) {
     gl_barrier();
-    flush(first, L.dec[(end - 1 - first) & 1].e);
+    flush(first, L.dec[(end - 1 - first) & 1].e, lane);
   }
-  if (seg == 0 && !dk_group) store_state_transposed<D>(x, a.dw0 + static_cast<size_t>(chain) * D * D, wv, g, r);
+  if (seg == 0 && !dk_group) store_state_transposed<IO, D>(x, a.dw0 + static_cast<size_t>(chain) * D * D, wv, g, r);
 }
 
 // dlog_gate from the per-token sums (see above): one wave per chunk, lane = token.  Each wave
