@@ -35,29 +35,9 @@ __device__ __forceinline__ gl_f4 keep4(float f, const gl_f4& x) {
 __device__ __forceinline__ float dot4(const gl_f4& a, const gl_f4& b) {
   return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
 }
-// over the four lanes (g) that share r: v_permlane32_swap and v_permlane16_swap of x with itself
-// leave the two halves' (rows') values side by side in two registers
-__device__ __forceinline__ float over_g(float x) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, x);
-  const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  const uint32_t a0 = h[0], a1 = h[1];
-  const uint32_t v = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a0) + __builtin_bit_cast(float, a1));
-  const auto w = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  const uint32_t b0 = w[0], b1 = w[1];
-  return __builtin_bit_cast(float, b0) + __builtin_bit_cast(float, b1);
-}
-
-// over the sixteen lanes (r) that share g, by rotations within the row
-template <int kShift>
-__device__ __forceinline__ float rotate(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + kShift, 0xF, 0xF, false));
-}
-__device__ __forceinline__ float over_r(float x) {
-  x += rotate<8>(x);
-  x += rotate<4>(x);
-  x += rotate<2>(x);
-  return x + rotate<1>(x);
-}
+// over the four lanes (g) that share r, and over the sixteen that share g
+__device__ __forceinline__ float over_g(float x) { return gl_swap16(gl_swap32(x)); }
+__device__ __forceinline__ float over_r(float x) { return gl_lane_sum<16>(x); }
 
 // Matrices in LDS hold a token (or a row of token pairs) per row.  Math<IO>: their element and
 // layout, and operands over 32 k (`Half`: over 16, when d = 16).
@@ -500,31 +480,39 @@ __global__ __launch_bounds__(4 * D) void gl_sums_kernel(GatedArgs a) {
 
 // The sums become the states at the segments' starts (side 0, first to last from w0) and the
 // gradients at their ends (side 1, last to first from dw_out), in place.
-// One element a thread; the sums of kAhead segments are loaded before the first is used.
-template <int D>
+// VEC elements a thread; the sums of kAhead segments are loaded before the first is used.
+template <int D, int VEC>
 __global__ __launch_bounds__(256) void gl_scan_kernel(GatedArgs a) {
-  constexpr int kAhead = 16;
-  const long long item = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  const int chain = static_cast<int>(item / (D * D)), at = static_cast<int>(item % (D * D)), side = blockIdx.y;
+  typedef float vec __attribute__((ext_vector_type(VEC)));
+  constexpr int kAhead = 8, kPer = D * D / VEC;  // threads per sequence
+  const int item = blockIdx.x * 256 + threadIdx.x;
+  const int chain = item / kPer, at = item % kPer * VEC, side = blockIdx.y;
+  if (chain >= a.B * a.H) return;
   const size_t seg0 = static_cast<size_t>(chain) * a.nseg;
   float* x = (side == 0 ? a.seg_w : a.seg_g) + seg0 * D * D + at;
   const float* decay = a.seg_decay + static_cast<size_t>(side) * a.B * a.H * a.nseg + seg0;
-  float state = side == 0 ? initial_state(a, chain, D * D)[at]
-                          : a.dw_out ? a.dw_out[static_cast<size_t>(chain) * D * D + at] : 0.0f;
+  const float* start = side == 0 ? initial_state(a, chain, D * D) : a.dw_out ? a.dw_out + static_cast<size_t>(chain) * D * D : nullptr;
+  vec state = 0.0f;
+  if (start) state = *reinterpret_cast<const vec*>(start + at);
   for (int i0 = 0; i0 < a.nseg; i0 += kAhead) {
-    float sum[kAhead], dec[kAhead];
+    vec sum[kAhead];
+    float dec[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j, m = side == 0 ? i : a.nseg - 1 - i;
-      const bool have = i + 1 < a.nseg;  // nothing follows the last
-      sum[j] = have ? x[static_cast<size_t>(m) * D * D] : 0.0f;
-      dec[j] = have ? decay[m] : 0.0f;
+      sum[j] = 0.0f;
+      dec[j] = 0.0f;
+      if (i + 1 < a.nseg) {  // nothing follows the last
+        sum[j] = *reinterpret_cast<const vec*>(x + static_cast<size_t>(m) * D * D);
+        dec[j] = decay[m];
+      }
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j, m = side == 0 ? i : a.nseg - 1 - i;
-      if (i < a.nseg) x[static_cast<size_t>(m) * D * D] = state;
-      state = gl_keep(dec[j], state) + sum[j];
+      if (i < a.nseg) *reinterpret_cast<vec*>(x + static_cast<size_t>(m) * D * D) = state;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) state[e] = gl_keep(dec[j], state[e]) + sum[j][e];
     }
   }
 }
@@ -977,43 +965,54 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
   if (seg == 0 && !dk_group) store_state_transposed<IO, D>(x, a.dw0 + static_cast<size_t>(chain) * D * D, wv, g, r);
 }
 
-// dlog_gate from the per-token sums (see above): one wave per chunk, lane = token.  Each wave
-// first walks the sums of the later chunks of its segment.
-__global__ __launch_bounds__(256) void gl_dgate_kernel(GatedArgs a, int nend) {
-  const int lane = threadIdx.x & 63;
+// dlog_gate from the per-token sums (see above): a workgroup per segment, a wave per chunk, lane =
+// token.  First every chunk's sum of in - out, then for each chunk the sums of the later ones.
+constexpr int kGateWaves = 8;
+__global__ __launch_bounds__(64 * kGateWaves) void gl_dgate_kernel(GatedArgs a, int nend) {
+  extern __shared__ double chunk_sum[];  // [spc]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int nchunks = (a.T + kC - 1) / kC;
-  const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (item >= static_cast<long long>(a.B) * a.H * nchunks) return;
-  const int chain = static_cast<int>(item / nchunks), c = static_cast<int>(item % nchunks), seg = c / a.spc;
+  const int chain = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
+  const int first = seg * a.spc, n = min(a.spc, nchunks - first);
   const size_t all = static_cast<size_t>(a.B) * a.H * a.T, row0 = static_cast<size_t>(chain) * a.T;
   const float* row = a.ws_tok + row0;
   const float* in = row + all;
   const float* col = in + all;
   const float* out = col + all;
   const int len = gl_length(a.lengths, chain / a.H, a.T);
-  const long long seg_end = static_cast<long long>(seg + 1) * a.spc * kC;
-  const int stop = seg_end < a.T ? static_cast<int>(seg_end) : a.T;
-  double later = 0.0;  // over the tokens of later chunks, and <G, W> at the segment's end
-  for (int t = (c + 1) * kC + lane; t < stop; t += 64) later += static_cast<double>(in[t]) - out[t];
-  if (lane < nend) later += a.ws_end[(static_cast<size_t>(chain) * a.nseg + seg) * nend + lane];
+  auto wave_sum = [](double x) {
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) later += __shfl_xor(later, o, 64);
-  const int t = c * kC + lane;
-  const bool have = t < a.T;
-  double suf = have ? static_cast<double>(row[t]) - col[t] + in[t] : 0.0;  // over u >= t
-  const double o_t = have ? static_cast<double>(out[t]) : 0.0;
-  double pre = o_t;  // over s <= t
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double x = __shfl_down(suf, o, 64), y = __shfl_up(pre, o, 64);
-    if (lane + o < 64) suf += x;
-    if (lane >= o) pre += y;
+    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
+    return x;
+  };
+  for (int c = wave; c < n; c += kGateWaves) {
+    const int t = (first + c) * kC + lane;
+    const double x = wave_sum(t < a.T ? static_cast<double>(in[t]) - out[t] : 0.0);
+    if (lane == 0) chunk_sum[c] = x;
   }
-  const double past = later - __shfl(pre, 63, 64);
-  if (!have) return;
-  // a token that forgets everything (decay 0) takes no gradient
-  const bool live = t < len && !(static_cast<double>(a.gate[row0 + t]) * 1.4426950408889634 <= kGlNever);
-  a.dgate[row0 + t] = live ? static_cast<float>(suf + (pre - o_t) + past) : 0.0f;
+  __syncthreads();
+  for (int c = wave; c < n; c += kGateWaves) {
+    // over the later chunks, and <G, W> at the segment's end
+    double later = lane < nend ? a.ws_end[static_cast<size_t>(blockIdx.x) * nend + lane] : 0.0;
+    for (int i = c + 1 + lane; i < n; i += 64) later += chunk_sum[i];
+    later = wave_sum(later);
+    const int t = (first + c) * kC + lane;
+    const bool have = t < a.T;
+    double suf = have ? static_cast<double>(row[t]) - col[t] + in[t] : 0.0;  // over u >= t
+    const double o_t = have ? static_cast<double>(out[t]) : 0.0;
+    double pre = o_t;  // over s <= t
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const double x = __shfl_down(suf, o, 64), y = __shfl_up(pre, o, 64);
+      if (lane + o < 64) suf += x;
+      if (lane >= o) pre += y;
+    }
+    const double past = later - __shfl(pre, 63, 64);
+    if (!have) continue;
+    // a token that forgets everything (decay 0) takes no gradient
+    const bool live = t < len && !(static_cast<double>(a.gate[row0 + t]) * 1.4426950408889634 <= kGlNever);
+    a.dgate[row0 + t] = live ? static_cast<float>(suf + (pre - o_t) + past) : 0.0f;
+  }
 }
 
 // ---------------------------------------------------------------- host
@@ -1022,7 +1021,7 @@ __global__ __launch_bounds__(256) void gl_dgate_kernel(GatedArgs a, int nend) {
 // workgroups run at once and each spends about kStart chunks' time before its first.
 void plan(GatedArgs* a, bool bwd) {
   constexpr int kStart = 2;
-  const int slots = getenv("GL_WANT") ? atoi(getenv("GL_WANT")) : bwd ? 512 : 768;
+  const int slots = bwd ? 512 : 768;
   const long long nchunks = (a->T + kC - 1) / kC, chains = static_cast<long long>(a->B) * a->H;
   long long best = -1;
   a->spc = 1;
@@ -1057,7 +1056,10 @@ hipError_t segment_states(const GatedArgs& a, int sides, hipStream_t s) {
   fn<<<dim3(chains * a.nseg, sides), dim3(4 * D), bytes, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  gl_scan_kernel<D><<<dim3(chains * (D * D / 256), sides), dim3(256), 0, s>>>(a);
+  // four elements a thread once that still fills the chip (256 CUs of 2048 threads)
+  const long long quads = static_cast<long long>(chains) * (D * D / 4) * sides;
+  if (quads >= 256 * 512) gl_scan_kernel<D, 4><<<dim3(static_cast<unsigned>((quads / sides + 255) / 256), sides), dim3(256), 0, s>>>(a);
+  else gl_scan_kernel<D, 1><<<dim3(chains * (D * D / 256), sides), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -1086,8 +1088,10 @@ hipError_t bwd(const GatedArgs& a, hipStream_t s) {
   dkv<<<dim3(groups), dim3(8 * D), dkv_bytes, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess || !a.dgate || a.T == 0) return e;
-  const long long items = static_cast<long long>(a.B) * a.H * ((a.T + kC - 1) / kC);
-  gl_dgate_kernel<<<dim3(static_cast<unsigned>((items + 3) / 4)), dim3(256), 0, s>>>(a, D / 16);
+  const int sums = a.spc * static_cast<int>(sizeof(double));
+  e = allow_lds(gl_dgate_kernel, sums);
+  if (e != hipSuccess) return e;
+  gl_dgate_kernel<<<dim3(groups), dim3(64 * kGateWaves), sums, s>>>(a, D / 16);
   return hipGetLastError();
 }
 

@@ -84,6 +84,49 @@ typedef float gl_f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t gl_u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t gl_u4 __attribute__((ext_vector_type(4)));
 
+// x plus the other half's (the neighbouring row's) x: v_permlane32_swap and v_permlane16_swap of x
+// with itself leave the two values side by side in two registers
+__device__ __forceinline__ float gl_swap32(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto y = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t a = y[0], b = y[1];
+  return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+}
+__device__ __forceinline__ float gl_swap16(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto y = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t a = y[0], b = y[1];
+  return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+}
+template <int kCtrl>
+__device__ __forceinline__ float gl_lane(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kCtrl, 0xF, 0xF, false));
+}
+// Sum over aligned groups of W lanes (a power of two), in every lane, without LDS: neighbours by
+// quad_perm, then the mirrored half row and row (their lanes hold equal sums), then swaps.
+template <int W>
+__device__ __forceinline__ float gl_lane_sum(float x) {
+  if constexpr (W >= 2) x += gl_lane<0xB1>(x);
+  if constexpr (W >= 4) x += gl_lane<0x4E>(x);
+  if constexpr (W >= 8) x += gl_lane<0x141>(x);
+  if constexpr (W >= 16) x += gl_lane<0x140>(x);
+  if constexpr (W >= 32) x = gl_swap16(x);
+  if constexpr (W >= 64) x = gl_swap32(x);
+  return x;
+}
+
+// Sum over the lanes of a wave that are equal modulo W, in every lane: rotations within the row of
+// 16, then swaps.
+template <int W>
+__device__ __forceinline__ float gl_stride_sum(float x) {
+  if constexpr (W <= 2) x += gl_lane<0x122>(x);
+  if constexpr (W <= 4) x += gl_lane<0x124>(x);
+  if constexpr (W <= 8) x += gl_lane<0x128>(x);
+  if constexpr (W <= 16) x = gl_swap16(x);
+  if constexpr (W <= 32) x = gl_swap32(x);
+  return x;
+}
+
 // Loads and stores through buffer resources whose range ends at the last valid token: rows
 // past it read as zero and their stores are dropped.  The range is the same in every lane; said
 // so, it stays in scalar registers (else each access is wrapped in a loop over the lanes' values).

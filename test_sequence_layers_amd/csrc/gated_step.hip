@@ -2,7 +2,7 @@
 //   W <- a W + e v k^T,  z = W q,  a = exp(g),  e = eta eta_tok.
 // Each state is read once and written once (2 d^2 floats a head); everything else is small, so
 // the kernel is bound by that traffic.  A thread holds four consecutive columns of its rows, a row
-// is spread over d / 4 neighbouring lanes, and z's sum over the columns is a shuffle among them.
+// is spread over d / 4 neighbouring lanes, and z's sum over the columns is a sum over neighbouring lanes.
 #include "gated_linear.hpp"
 
 namespace ttt {
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void gl_step_kernel(GatedArgs a, float* w) {
       sum += x[i][c] * q[c];
     }
     *reinterpret_cast<gl_f4*>(wc + i * kRows * D) = x[i];
-    sum = group_sum<D / 4>(sum);
+    sum = gl_lane_sum<D / 4>(sum);
     if (col == 0) z[i * kRows] = from_f32<IO>(sum);
   }
 }

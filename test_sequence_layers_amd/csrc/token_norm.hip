@@ -89,7 +89,7 @@ __device__ __forceinline__ void act_grad(int act, float g, float* a, float* da) 
 // wave, used alternately so that one barrier a sum is enough).
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x, float (*red)[16], int* turn) {
-  x = group_sum<(LPR < 64 ? LPR : 64)>(x);
+  x = gl_lane_sum<(LPR < 64 ? LPR : 64)>(x);
   if constexpr (LPR > 64) {
     float* slot = red[*turn & 1];
     ++*turn;
@@ -195,18 +195,19 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_fwd_kernel(NormArgs
   }
 }
 
-// Workgroup (part, head) takes an even share of the head's B T rows, and leaves its sums of the
-// parameters' gradients in part[head][part][3][d].
+// Workgroup (part, head) takes a share of the head's B T rows, and leaves its sums of the
+// parameters' gradients in part[head][part][wanted sums][d].
 template <typename IO, int W, int LPR, int NV>
-__global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs a, float* part) {
-  extern __shared__ float sums[];  // [3][d] (rows of a wave or less)
+__global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs a, float* part, int share) {
+  extern __shared__ __attribute__((aligned(16))) float sums[];  // [2][wanted sums][d] (rows of a wave or less)
   __shared__ float red[2][16];
   int turn = 0;
   constexpr int RB = Block<LPR>::kRows, N = NV * W;
   const int in_row = threadIdx.x % LPR, group = threadIdx.x / LPR;
   const int head = blockIdx.y;
   const long long all = static_cast<long long>(a.B) * a.T;  // at most 2^30
-  const int from = static_cast<int>(all * blockIdx.x / gridDim.x), to = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
+  const int from = static_cast<int>(blockIdx.x) * share;  // below all
+  const int to = static_cast<int>(all - from < share ? all : from + share);
   const IO* xp = static_cast<const IO*>(a.x);
   const IO* gp = static_cast<const IO*>(a.gate);
   const IO* dyp = static_cast<const IO*>(a.dy);
@@ -308,52 +309,55 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
     }
   }
   if (!part) return;
-  // rows of one workgroup: lanes that hold the same columns, then wave after wave
+  // over the lanes that hold the same columns, then over the waves in a tree through LDS
   if constexpr (LPR < 64) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-#pragma unroll
-      for (int o = LPR; o < 64; o <<= 1) {
-        sw[i] += __shfl_xor(sw[i], o, 64);
-        sb[i] += __shfl_xor(sb[i], o, 64);
-        ss[i] += __shfl_xor(ss[i], o, 64);
-      }
+      sw[i] = gl_stride_sum<LPR>(sw[i]);
+      sb[i] = gl_stride_sum<LPR>(sb[i]);
+      ss[i] = gl_stride_sum<LPR>(ss[i]);
     }
   }
-  float* out = part + (static_cast<size_t>(head) * gridDim.x + blockIdx.x) * 3 * a.d;
-  if constexpr (LPR > 64) {  // one row at a time: the registers hold the workgroup's sums
+  // [wanted sums][d], those of weight, bias and scale in order
+  const int nw = a.dweight ? 1 : 0, nb = a.dbias ? 1 : 0, ns = a.dscale ? 1 : 0, all_sums = (nw + nb + ns) * a.d;
+  constexpr int P = W < 4 ? W : 4;  // floats at a time
+  typedef float piece __attribute__((ext_vector_type(P)));
+  auto pieces = [&](int at, float* x, auto f) {
+#pragma unroll
+    for (int i = 0; i < W; i += P) {
+      piece y;
+#pragma unroll
+      for (int j = 0; j < P; ++j) y[j] = x[i + j];
+      f(at + i, y);
+#pragma unroll
+      for (int j = 0; j < P; ++j) x[i + j] = y[j];
+    }
+  };
+  auto columns = [&](auto f) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int col = (v * LPR + in_row) * W;
-      if (col < a.d) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          out[col + i] = sw[v * W + i];
-          out[a.d + col + i] = sb[v * W + i];
-          out[2 * a.d + col + i] = ss[v * W + i];
-        }
-      }
+      if (col >= a.d) continue;
+      if (nw) pieces(col, sw + v * W, f);
+      if (nb) pieces(nw * a.d + col, sb + v * W, f);
+      if (ns) pieces((nw + nb) * a.d + col, ss + v * W, f);
     }
-  } else {
-    for (int w = 0; w < Block<LPR>::kThreads / 64; ++w) {
-      if (static_cast<int>(threadIdx.x & 63) < LPR && static_cast<int>(threadIdx.x >> 6) == w) {
+  };
+  const int wave = threadIdx.x >> 6;
+  const bool mine = LPR >= 64 || static_cast<int>(threadIdx.x & 63) < LPR;
+  if constexpr (LPR <= 64) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int col = (v * LPR + in_row) * W;
-          if (col < a.d) {
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-              const int j = v * W + i;
-              sums[col + i] = w ? sums[col + i] + sw[j] : sw[j];
-              sums[a.d + col + i] = w ? sums[a.d + col + i] + sb[j] : sb[j];
-              sums[2 * a.d + col + i] = w ? sums[2 * a.d + col + i] + ss[j] : ss[j];
-            }
-          }
-        }
-      }
+    for (int half = Block<LPR>::kThreads / 128; half > 0; half >>= 1) {
+      float* slot = sums + (wave % half) * all_sums;
+      if (mine && wave >= half && wave < 2 * half) columns([&](int at, piece& x) { *reinterpret_cast<piece*>(slot + at) = x; });
+      __syncthreads();
+      if (mine && wave < half) columns([&](int at, piece& x) { x += *reinterpret_cast<const piece*>(slot + at); });
       __syncthreads();
     }
-    for (int i = threadIdx.x; i < 3 * a.d; i += Block<LPR>::kThreads) out[i] = sums[i];
+  }
+  if (LPR > 64 || (mine && wave == 0)) {
+    float* out = part + (static_cast<size_t>(head) * gridDim.x + blockIdx.x) * all_sums;
+    columns([&](int at, piece& x) { *reinterpret_cast<piece*>(out + at) = x; });
   }
 }
 
@@ -368,9 +372,11 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs a, const float*
   if (!out) return;
   double s = 0.0;
   if (col < a.d) {
-    const float* p = part + static_cast<size_t>(head) * parts * 3 * a.d + static_cast<size_t>(which) * a.d + col;
+    const int before[3] = {0, a.dweight ? 1 : 0, (a.dweight ? 1 : 0) + (a.dbias ? 1 : 0)};
+    const size_t pitch = static_cast<size_t>(before[2] + (a.dscale ? 1 : 0)) * a.d;
+    const float* p = part + static_cast<size_t>(head) * parts * pitch + static_cast<size_t>(before[which]) * a.d + col;
 #pragma unroll 8
-    for (int i = q; i < parts; i += 32) s += p[static_cast<size_t>(i) * 3 * a.d];
+    for (int i = q; i < parts; i += 32) s += p[i * pitch];
   }
   share[q][c] = s;
   __syncthreads();
@@ -434,22 +440,37 @@ hipError_t run_fwd(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Shares of a head's rows in the backward pass: workgroups enough to fill the chip (about 1024),
-// each with 16 rows at least so that its sums stay small next to its rows.
-int bwd_parts(int B, int H, int T) {
+// The backward pass's workgroups: at most 768 (three of 256 threads a CU, so that all start at
+// once and end together), each with 16 rows of a head at least so that its sums stay small next to
+// its rows.  On 8 x 12 x 2048 rows of 64 bf16: 512 workgroups 33.5 us, 768 28.5, 1024 34.7, 1536 31.2;
+// on 8191 rows of 768: 256 workgroups 20.2 us, 512 16.3, 1024 18.7.
+long long most_parts(int B, int H, int T) {
   const long long rows = static_cast<long long>(B) * T;
-  long long parts = (1024 + H - 1) / H;
+  long long parts = 768 / H;
   if (parts > (rows + 15) / 16) parts = (rows + 15) / 16;
+  return parts < 1 ? 1 : parts;
+}
+// rows of a part: whole passes of `at_once` rows
+int rows_of_part(int B, int H, int T, int at_once) {
+  const long long rows = static_cast<long long>(B) * T, parts = most_parts(B, H, T);
+  const long long share = (rows + parts - 1) / parts;
+  return static_cast<int>(share < 1 ? at_once : (share + at_once - 1) / at_once * at_once);
+}
+int bwd_parts(int B, int H, int T, int share) {
+  const long long rows = static_cast<long long>(B) * T, parts = (rows + share - 1) / share;
   return static_cast<int>(parts < 1 ? 1 : parts);
 }
 
 template <typename IO, int W, int LPR, int NV>
 hipError_t run_bwd(const NormArgs& a, void* ws, hipStream_t s) {
-  const int parts = bwd_parts(a.B, a.H, a.T);
+  const int share = rows_of_part(a.B, a.H, a.T, Block<LPR>::kRows), parts = bwd_parts(a.B, a.H, a.T, share);
   const bool sums = a.dweight || a.dbias || a.dscale;
-  const int lds = sums && LPR <= 64 ? 3 * a.d * static_cast<int>(sizeof(float)) : 0;  // 24 KB at most
-  const auto fn = norm_bwd_kernel<IO, W, LPR, NV>;
-  fn<<<dim3(parts, a.H), dim3(Block<LPR>::kThreads), lds, s>>>(a, sums ? static_cast<float*>(ws) : nullptr);
+  const int lds = sums && LPR <= 64 ? 2 * 3 * a.d * static_cast<int>(sizeof(float)) : 0;  // 48 KB at most
+  float* part = sums ? static_cast<float*>(ws) : nullptr;
+  norm_bwd_kernel<IO, W, LPR, NV><<<dim3(parts, a.H), dim3(Block<LPR>::kThreads), lds, s>>>(a, part, share);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !sums) return e;
+  norm_sum_kernel<<<dim3((a.d + 31) / 32, a.H, 3), dim3(1024), 0, s>>>(a, part, parts);
   return hipGetLastError();
 }
 
@@ -457,10 +478,7 @@ template <typename IO>
 hipError_t bwd_io(const NormArgs& a, void* ws, hipStream_t s) {
   auto go = [&](auto w, auto lpr, auto nv) { return run_bwd<IO, w.value, lpr.value, nv.value>(a, ws, s); };
   constexpr int W = 16 / static_cast<int>(sizeof(IO));
-  hipError_t e = vectors(a, sizeof(IO)) ? layout<W>(a.d, go) : layout<1>(a.d, go);
-  if (e != hipSuccess || !(a.dweight || a.dbias || a.dscale)) return e;
-  norm_sum_kernel<<<dim3((a.d + 31) / 32, a.H, 3), dim3(1024), 0, s>>>(a, static_cast<const float*>(ws), bwd_parts(a.B, a.H, a.T));
-  return hipGetLastError();
+  return vectors(a, sizeof(IO)) ? layout<W>(a.d, go) : layout<1>(a.d, go);
 }
 
 template <typename IO>
@@ -473,7 +491,7 @@ hipError_t fwd_io(const NormArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t token_norm_bwd_workspace_bytes(int B, int H, int T, int d) {
-  return static_cast<size_t>(bwd_parts(B, H, T)) * H * 3 * d * sizeof(float);
+  return static_cast<size_t>(most_parts(B, H, T)) * H * 3 * d * sizeof(float);
 }
 
 hipError_t launch_token_norm_fwd(const NormArgs& a, bool bf16_io, hipStream_t s) {
