@@ -1021,6 +1021,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gl_dgate_kernel(GatedArgs a, 
 // workgroups run at once and each spends about kStart chunks' time before its first.
 void plan(GatedArgs* a, bool bwd) {
   constexpr int kStart = 2;
+  const int launches = bwd ? 1 : 3;  // chunks' time that the two more launches take
   const int slots = bwd ? 512 : 768;
   const long long nchunks = (a->T + kC - 1) / kC, chains = static_cast<long long>(a->B) * a->H;
   long long best = -1;
@@ -1029,7 +1030,7 @@ void plan(GatedArgs* a, bool bwd) {
   for (long long n = 1; n <= nchunks && n <= 512; ++n) {
     const long long spc = (nchunks + n - 1) / n, nseg = (nchunks + spc - 1) / spc;
     if (nseg < n) continue;  // as many segments come from a smaller n
-    const long long cost = (chains * nseg + slots - 1) / slots * (spc + kStart);
+    const long long cost = (chains * nseg + slots - 1) / slots * (spc + kStart) + (nseg > 1 ? launches : 0);
     if (best < 0 || cost < best) {
       best = cost;
       a->spc = static_cast<int>(spc);

@@ -13,8 +13,14 @@
 // Both are bound by HBM: each tensor passes once.  A row lives in the registers of LPR lanes
 // (part of a wave, a wave, or a workgroup), NV vectors of W elements a lane, so its statistics
 // need no second read; everything between load and store is float32.
+//
+// A vector is 16 bytes.  Where rows or tensors are not aligned to that (`A` false) its loads and
+// stores are not either, and the last vector of a row begins early, at d - W: its first `dup`
+// elements belong to the lane before and count as absent.  (One element a load took 82 us on 2604
+// rows of 4751 bf16 with gate and residual, this takes 35.)
 #include <initializer_list>
 #include <type_traits>
+#include <utility>
 
 #include "gated_linear.hpp"
 
@@ -24,47 +30,70 @@ namespace {
 enum { kLayer = 0, kRms = 1, kL2 = 2 };
 enum { kActNone = 0, kSilu = 1, kGelu = 2, kSigmoid = 3 };
 
-// W consecutive elements (16 bytes, or one) as they are loaded
-template <typename IO, int W>
+// W consecutive elements as they are loaded
+template <typename IO, int W, bool A>
 struct Vec {
   typedef IO type __attribute__((ext_vector_type(W)));
   type v;
   __device__ __forceinline__ void load(const IO* p) {
     if constexpr (W == 1) v[0] = p[0];
-    else v = *reinterpret_cast<const type*>(p);
+    else if constexpr (A) v = *reinterpret_cast<const type*>(p);
+    else __builtin_memcpy(&v, p, sizeof(v));
   }
-  __device__ __forceinline__ void widen(float* x, bool have) const {
+  __device__ __forceinline__ void widen(float* x, bool have, int dup) const {
 #pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = have ? to_f32(static_cast<IO>(v[i])) : 0.0f;
+    for (int i = 0; i < W; ++i) x[i] = have && (A || i >= dup) ? to_f32(static_cast<IO>(v[i])) : 0.0f;
   }
 };
-template <typename IO, int W>
-__device__ __forceinline__ void load_vec(const IO* p, float* x) {
-  Vec<IO, W> v;
-  v.load(p);
-  v.widen(x, true);
-}
-template <typename IO, int W>
-__device__ __forceinline__ void store_vec(IO* p, const float* x) {
+template <typename IO, int W, bool A>
+__device__ __forceinline__ void store_vec(IO* p, const float* x, int dup) {
   if constexpr (W == 1) {
     p[0] = from_f32<IO>(x[0]);
   } else {
-    typedef IO vec __attribute__((ext_vector_type(W)));
-    vec y;
+    typename Vec<IO, W, A>::type y;
 #pragma unroll
     for (int i = 0; i < W; ++i) y[i] = from_f32<IO>(x[i]);
-    *reinterpret_cast<vec*>(p) = y;
+    if constexpr (A) {
+      *reinterpret_cast<typename Vec<IO, W, A>::type*>(p) = y;
+    } else if (dup == 0) {
+      __builtin_memcpy(p, &y, sizeof(y));
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (i >= dup) p[i] = y[i];
+    }
   }
 }
-// float32 parameters of the same W columns (16-byte loads when W > 1)
-template <int W>
+// where a lane's vector v begins in its row
+template <int W, int LPR, bool A>
+struct Place {
+  int col, dup;
+  bool have;
+  __device__ __forceinline__ Place(int v, int in_row, int d) {
+    const int at = (v * LPR + in_row) * W;
+    have = at < d;
+    col = !have ? 0 : A ? at : min(at, d - W);
+    dup = have ? at - col : 0;
+  }
+};
+template <int W, int LPR, int NV, bool A>
+struct Places {
+  Place<W, LPR, A> p[NV];
+  __device__ __forceinline__ Places(int in_row, int d) : Places(in_row, d, std::make_integer_sequence<int, NV>()) {}
+  template <int... V>
+  __device__ __forceinline__ Places(int in_row, int d, std::integer_sequence<int, V...>) : p{Place<W, LPR, A>(V, in_row, d)...} {}
+};
+// float32 parameters of the same W columns (16 bytes at a time when W > 1)
+template <int W, bool A>
 __device__ __forceinline__ void load_par(const float* p, float* x) {
   if constexpr (W == 1) {
     x[0] = p[0];
   } else {
 #pragma unroll
     for (int i = 0; i < W; i += 4) {
-      const gl_f4 y = *reinterpret_cast<const gl_f4*>(p + i);
+      gl_f4 y;
+      if constexpr (A) y = *reinterpret_cast<const gl_f4*>(p + i);
+      else __builtin_memcpy(&y, p + i, sizeof(y));
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[i + j] = y[j];
     }
@@ -103,9 +132,10 @@ __device__ __forceinline__ float row_sum(float x, float (*red)[16], int* turn) {
 }
 
 // The row in registers: x becomes xh; returns r.
-template <int LPR, int N>
-__device__ __forceinline__ float normalise(float* x, const bool* have, int W, int kind, int d, float eps,
+template <int W, int LPR, int NV, bool A>
+__device__ __forceinline__ float normalise(float* x, const bool* live, const Place<W, LPR, A>* at, int kind, int d, float eps,
                                            float (*red)[16], int* turn) {
+  constexpr int N = NV * W;
   const float inv = kind == kL2 ? 1.0f : 1.0f / d;
   if (kind == kLayer) {
     float sum = 0.0f;
@@ -113,7 +143,7 @@ __device__ __forceinline__ float normalise(float* x, const bool* have, int W, in
     for (int i = 0; i < N; ++i) sum += x[i];
     const float m = row_sum<LPR>(sum, red, turn) * inv;
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = have[i / W] ? x[i] - m : 0.0f;
+    for (int i = 0; i < N; ++i) x[i] = live[i / W] && (A || i % W >= at[i / W].dup) ? x[i] - m : 0.0f;
   }
   float ss = 0.0f;
 #pragma unroll
@@ -130,7 +160,7 @@ template <int LPR> struct Block {
 };
 
 // A workgroup takes `passes` x kRows consecutive rows.
-template <typename IO, int W, int LPR, int NV>
+template <typename IO, int W, int LPR, int NV, bool A>
 __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_fwd_kernel(NormArgs a, int rows, int passes) {
   __shared__ float red[2][16];
   int turn = 0;
@@ -140,6 +170,8 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_fwd_kernel(NormArgs
   const IO* gp = static_cast<const IO*>(a.gate);
   const IO* rp = static_cast<const IO*>(a.res);
   IO* yp = static_cast<IO*>(a.y);
+  const Places<W, LPR, NV, A> places(in_row, a.d);
+  const Place<W, LPR, A>* at = places.p;
   for (int p = 0; p < passes; ++p) {
     const long long first = (static_cast<long long>(blockIdx.x) * passes + p) * RB;
     if (first >= rows) return;  // the same for every thread
@@ -151,31 +183,33 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_fwd_kernel(NormArgs
     bool have[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int col = (v * LPR + in_row) * W;
-      have[v] = live && col < a.d;
+      const int col = at[v].col;
+      have[v] = live && at[v].have;
+      Vec<IO, W, A> lx, lg, lr;
+      lx.load(xp + base + col);
+      if (gp) lg.load(gp + base + col);
+      if (rp) lr.load(rp + base + col);
+      lx.widen(x + v * W, have[v], at[v].dup);
 #pragma unroll
-      for (int i = 0; i < W; ++i) x[v * W + i] = gt[v * W + i] = rs[v * W + i] = 0.0f;
-      if (have[v]) {
-        load_vec<IO, W>(xp + base + col, x + v * W);
-        if (gp) load_vec<IO, W>(gp + base + col, gt + v * W);
-        if (rp) load_vec<IO, W>(rp + base + col, rs + v * W);
-      }
+      for (int i = 0; i < W; ++i) gt[v * W + i] = rs[v * W + i] = 0.0f;
+      if (gp) lg.widen(gt + v * W, true, 0);
+      if (rp) lr.widen(rs + v * W, true, 0);
     }
-    normalise<LPR, NV * W>(x, have, W, a.kind, a.d, a.eps, red, &turn);
+    normalise<W, LPR, NV, A>(x, have, at, a.kind, a.d, a.eps, red, &turn);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (!have[v]) continue;
-      const int col = (v * LPR + in_row) * W;
+      const int col = at[v].col;
       float par[W], y[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) y[i] = x[v * W + i];
       if (a.weight) {
-        load_par<W>(a.weight + hb + col, par);
+        load_par<W, A>(a.weight + hb + col, par);
 #pragma unroll
         for (int i = 0; i < W; ++i) y[i] *= par[i];
       }
       if (a.bias) {
-        load_par<W>(a.bias + hb + col, par);
+        load_par<W, A>(a.bias + hb + col, par);
 #pragma unroll
         for (int i = 0; i < W; ++i) y[i] += par[i];
       }
@@ -184,20 +218,20 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_fwd_kernel(NormArgs
         for (int i = 0; i < W; ++i) y[i] *= act_(a.act, gt[v * W + i]);
       }
       if (a.scale) {
-        load_par<W>(a.scale + hb + col, par);
+        load_par<W, A>(a.scale + hb + col, par);
 #pragma unroll
         for (int i = 0; i < W; ++i) y[i] *= par[i];
       }
 #pragma unroll
       for (int i = 0; i < W; ++i) y[i] += rs[v * W + i];
-      store_vec<IO, W>(yp + base + col, y);
+      store_vec<IO, W, A>(yp + base + col, y, at[v].dup);
     }
   }
 }
 
 // Workgroup (part, head) takes a share of the head's B T rows, and leaves its sums of the
 // parameters' gradients in part[head][part][wanted sums][d].
-template <typename IO, int W, int LPR, int NV>
+template <typename IO, int W, int LPR, int NV, bool A>
 __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs a, float* part, int share) {
   extern __shared__ __attribute__((aligned(16))) float sums[];  // [2][wanted sums][d] (rows of a wave or less)
   __shared__ float red[2][16];
@@ -217,9 +251,11 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
   float sw[N], sb[N], ss[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) sw[i] = sb[i] = ss[i] = 0.0f;
+  const Places<W, LPR, NV, A> places(in_row, a.d);
+  const Place<W, LPR, A>* at = places.p;
   // a row as it is loaded; that of the next turn is on its way while one is worked on
   struct Row {
-    Vec<IO, W> x[NV], dy[NV], gt[NV];
+    Vec<IO, W, A> x[NV], dy[NV], gt[NV];
     size_t base;
     bool live;
   } next;
@@ -229,7 +265,7 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
     next.base = (static_cast<size_t>(b * static_cast<unsigned>(a.H) + head) * a.T + (bt - b * static_cast<unsigned>(a.T))) * a.d;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int at = (v * LPR + in_row) * W, col = at < a.d ? at : 0;
+      const int col = at[v].col;
       next.x[v].load(xp + next.base + col);
       next.dy[v].load(dyp + next.base + col);
       if (gp) next.gt[v].load(gp + next.base + col);
@@ -237,7 +273,7 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
   };
   if (from < to) fetch(from);
   // the head's parameters, kept in registers while they are few
-  constexpr bool kKeep = N <= 16;
+  constexpr bool kKeep = N <= 24;
   float wt_[kKeep ? N : W], bs_[kKeep ? N : W], sc_[kKeep ? N : W];
   auto parameters = [&](int col, float* wt, float* bs, float* sc) {
 #pragma unroll
@@ -245,16 +281,13 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
       wt[i] = sc[i] = 1.0f;
       bs[i] = 0.0f;
     }
-    if (a.weight) load_par<W>(a.weight + hb + col, wt);
-    if (a.bias) load_par<W>(a.bias + hb + col, bs);
-    if (a.scale) load_par<W>(a.scale + hb + col, sc);
+    if (a.weight) load_par<W, A>(a.weight + hb + col, wt);
+    if (a.bias) load_par<W, A>(a.bias + hb + col, bs);
+    if (a.scale) load_par<W, A>(a.scale + hb + col, sc);
   };
   if constexpr (kKeep) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int at = (v * LPR + in_row) * W;
-      parameters(at < a.d ? at : 0, wt_ + v * W, bs_ + v * W, sc_ + v * W);
-    }
+    for (int v = 0; v < NV; ++v) parameters(at[v].col, wt_ + v * W, bs_ + v * W, sc_ + v * W);
   }
   for (int first = from; first < to; first += RB) {
     const size_t base = next.base;
@@ -262,18 +295,18 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
     bool have[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      have[v] = next.live && (v * LPR + in_row) * W < a.d;
-      next.x[v].widen(x + v * W, have[v]);
-      next.dy[v].widen(dy + v * W, have[v]);
-      if (gp) next.gt[v].widen(gt + v * W, have[v]);
+      have[v] = next.live && at[v].have;
+      next.x[v].widen(x + v * W, have[v], at[v].dup);
+      next.dy[v].widen(dy + v * W, have[v], at[v].dup);
+      if (gp) next.gt[v].widen(gt + v * W, have[v], at[v].dup);
     }
     if (first + RB < to) fetch(first + RB);
-    const float r = normalise<LPR, N>(x, have, W, a.kind, a.d, a.eps, red, &turn);
+    const float r = normalise<W, LPR, NV, A>(x, have, at, a.kind, a.d, a.eps, red, &turn);
     float m1 = 0.0f, m2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (!have[v]) continue;
-      const int col = (v * LPR + in_row) * W;
+      const int col = at[v].col;
       float* wt = wt_ + (kKeep ? v * W : 0);
       float* bs = bs_ + (kKeep ? v * W : 0);
       float* sc = sc_ + (kKeep ? v * W : 0);
@@ -294,7 +327,7 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
         m1 += dy[j];
         m2 += dy[j] * x[j];
       }
-      if (dgp) store_vec<IO, W>(dgp + base + col, dg);
+      if (dgp) store_vec<IO, W, A>(dgp + base + col, dg, at[v].dup);
     }
     const float inv = 1.0f / a.d;
     m2 = row_sum<LPR>(m2, red, &turn) * (a.kind == kL2 ? 1.0f : inv);
@@ -305,7 +338,7 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
       float dx[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) dx[i] = r * (dy[v * W + i] - m1 - x[v * W + i] * m2);
-      store_vec<IO, W>(dxp + base + (v * LPR + in_row) * W, dx);
+      store_vec<IO, W, A>(dxp + base + at[v].col, dx, at[v].dup);
     }
   }
   if (!part) return;
@@ -320,15 +353,16 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
   }
   // [wanted sums][d], those of weight, bias and scale in order
   const int nw = a.dweight ? 1 : 0, nb = a.dbias ? 1 : 0, ns = a.dscale ? 1 : 0, all_sums = (nw + nb + ns) * a.d;
-  constexpr int P = W < 4 ? W : 4;  // floats at a time
+  constexpr int P = W < 4 || !A ? 1 : 4;  // floats at a time
   typedef float piece __attribute__((ext_vector_type(P)));
-  auto pieces = [&](int at, float* x, auto f) {
+  auto pieces = [&](int first, float* x, int dup, auto f) {
 #pragma unroll
     for (int i = 0; i < W; i += P) {
+      if (!A && i < dup) continue;
       piece y;
 #pragma unroll
       for (int j = 0; j < P; ++j) y[j] = x[i + j];
-      f(at + i, y);
+      f(first + i, y);
 #pragma unroll
       for (int j = 0; j < P; ++j) x[i + j] = y[j];
     }
@@ -336,11 +370,11 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
   auto columns = [&](auto f) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int col = (v * LPR + in_row) * W;
-      if (col >= a.d) continue;
-      if (nw) pieces(col, sw + v * W, f);
-      if (nb) pieces(nw * a.d + col, sb + v * W, f);
-      if (ns) pieces((nw + nb) * a.d + col, ss + v * W, f);
+      if (!at[v].have) continue;
+      const int col = at[v].col, dup = at[v].dup;
+      if (nw) pieces(col, sw + v * W, dup, f);
+      if (nb) pieces(nw * a.d + col, sb + v * W, dup, f);
+      if (ns) pieces((nw + nb) * a.d + col, ss + v * W, dup, f);
     }
   };
   const int wave = threadIdx.x >> 6;
@@ -349,15 +383,15 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
 #pragma unroll
     for (int half = Block<LPR>::kThreads / 128; half > 0; half >>= 1) {
       float* slot = sums + (wave % half) * all_sums;
-      if (mine && wave >= half && wave < 2 * half) columns([&](int at, piece& x) { *reinterpret_cast<piece*>(slot + at) = x; });
+      if (mine && wave >= half && wave < 2 * half) columns([&](int i, piece& x) { *reinterpret_cast<piece*>(slot + i) = x; });
       __syncthreads();
-      if (mine && wave < half) columns([&](int at, piece& x) { x += *reinterpret_cast<const piece*>(slot + at); });
+      if (mine && wave < half) columns([&](int i, piece& x) { x += *reinterpret_cast<const piece*>(slot + i); });
       __syncthreads();
     }
   }
   if (LPR > 64 || (mine && wave == 0)) {
     float* out = part + (static_cast<size_t>(head) * gridDim.x + blockIdx.x) * all_sums;
-    columns([&](int at, piece& x) { *reinterpret_cast<piece*>(out + at) = x; });
+    columns([&](int i, piece& x) { *reinterpret_cast<piece*>(out + i) = x; });
   }
 }
 
@@ -404,38 +438,44 @@ hipError_t layout(int d, F f) {
   const int n = (d + W - 1) / W;
 #define TTT_TRY(lpr, nv) \
   if (n <= lpr * nv) return f(std::integral_constant<int, W>(), std::integral_constant<int, lpr>(), std::integral_constant<int, nv>())
+  TTT_TRY(2, 1);
+  TTT_TRY(4, 1);
+  TTT_TRY(8, 1);
   if constexpr (W > 1) {
-    TTT_TRY(2, 1);
-    TTT_TRY(4, 1);
-    TTT_TRY(8, 1);
     TTT_TRY(16, 1);
     TTT_TRY(32, 1);
-  }
-  TTT_TRY(64, 1);
-  TTT_TRY(64, 2);
-  TTT_TRY(64, 4);
-  if constexpr (W == 1) TTT_TRY(64, 8);
-  TTT_TRY(256, 2);
-  TTT_TRY(256, 4);
-  if constexpr (W <= 4) TTT_TRY(256, 8);
-  if constexpr (W == 8) TTT_TRY(1024, 2);
-  TTT_TRY(1024, 4);
-  if constexpr (W == 1) {
-    TTT_TRY(1024, 8);
-    TTT_TRY(1024, 16);
+    TTT_TRY(64, 1);
+    TTT_TRY(32, 3);
+    TTT_TRY(64, 2);
+    TTT_TRY(64, 3);
+    TTT_TRY(64, 4);
+    TTT_TRY(256, 2);
+    TTT_TRY(256, 3);
+    TTT_TRY(256, 4);
+    if constexpr (W == 4) TTT_TRY(256, 8);
+    if constexpr (W == 8) TTT_TRY(1024, 2);
+    if constexpr (W == 4) TTT_TRY(1024, 4);
   }
 #undef TTT_TRY
   return hipErrorInvalidValue;
 }
+// whole rows of aligned vectors, else vectors at any element, else (rows shorter than one) elements
+template <typename IO, typename F>
+hipError_t choose(const NormArgs& a, F f) {
+  constexpr int W = 16 / static_cast<int>(sizeof(IO));
+  if (vectors(a, sizeof(IO))) return layout<W>(a.d, [&](auto w, auto lpr, auto nv) { return f(w, lpr, nv, std::true_type()); });
+  if (a.d >= W) return layout<W>(a.d, [&](auto w, auto lpr, auto nv) { return f(w, lpr, nv, std::false_type()); });
+  return layout<1>(a.d, [&](auto w, auto lpr, auto nv) { return f(w, lpr, nv, std::true_type()); });
+}
 
-template <typename IO, int W, int LPR, int NV>
+template <typename IO, int W, int LPR, int NV, bool A>
 hipError_t run_fwd(const NormArgs& a, hipStream_t s) {
   constexpr int RB = Block<LPR>::kRows;
   const long long rows = static_cast<long long>(a.B) * a.H * a.T;
   const long long groups = (rows + RB - 1) / RB;
   // several passes share a workgroup's start once there are workgroups enough
   const int passes = groups >= 8192 ? 4 : groups >= 4096 ? 2 : 1;
-  norm_fwd_kernel<IO, W, LPR, NV><<<dim3(static_cast<unsigned>((groups + passes - 1) / passes)), dim3(Block<LPR>::kThreads), 0, s>>>(
+  norm_fwd_kernel<IO, W, LPR, NV, A><<<dim3(static_cast<unsigned>((groups + passes - 1) / passes)), dim3(Block<LPR>::kThreads), 0, s>>>(
       a, static_cast<int>(rows), passes);
   return hipGetLastError();
 }
@@ -461,13 +501,13 @@ int bwd_parts(int B, int H, int T, int share) {
   return static_cast<int>(parts < 1 ? 1 : parts);
 }
 
-template <typename IO, int W, int LPR, int NV>
+template <typename IO, int W, int LPR, int NV, bool A>
 hipError_t run_bwd(const NormArgs& a, void* ws, hipStream_t s) {
   const int share = rows_of_part(a.B, a.H, a.T, Block<LPR>::kRows), parts = bwd_parts(a.B, a.H, a.T, share);
   const bool sums = a.dweight || a.dbias || a.dscale;
   const int lds = sums && LPR <= 64 ? 2 * 3 * a.d * static_cast<int>(sizeof(float)) : 0;  // 48 KB at most
   float* part = sums ? static_cast<float*>(ws) : nullptr;
-  norm_bwd_kernel<IO, W, LPR, NV><<<dim3(parts, a.H), dim3(Block<LPR>::kThreads), lds, s>>>(a, part, share);
+  norm_bwd_kernel<IO, W, LPR, NV, A><<<dim3(parts, a.H), dim3(Block<LPR>::kThreads), lds, s>>>(a, part, share);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !sums) return e;
   norm_sum_kernel<<<dim3((a.d + 31) / 32, a.H, 3), dim3(1024), 0, s>>>(a, part, parts);
@@ -476,16 +516,12 @@ hipError_t run_bwd(const NormArgs& a, void* ws, hipStream_t s) {
 
 template <typename IO>
 hipError_t bwd_io(const NormArgs& a, void* ws, hipStream_t s) {
-  auto go = [&](auto w, auto lpr, auto nv) { return run_bwd<IO, w.value, lpr.value, nv.value>(a, ws, s); };
-  constexpr int W = 16 / static_cast<int>(sizeof(IO));
-  return vectors(a, sizeof(IO)) ? layout<W>(a.d, go) : layout<1>(a.d, go);
+  return choose<IO>(a, [&](auto w, auto lpr, auto nv, auto al) { return run_bwd<IO, w.value, lpr.value, nv.value, al.value>(a, ws, s); });
 }
 
 template <typename IO>
 hipError_t fwd_io(const NormArgs& a, hipStream_t s) {
-  auto go = [&](auto w, auto lpr, auto nv) { return run_fwd<IO, w.value, lpr.value, nv.value>(a, s); };
-  constexpr int W = 16 / static_cast<int>(sizeof(IO));
-  return vectors(a, sizeof(IO)) ? layout<W>(a.d, go) : layout<1>(a.d, go);
+  return choose<IO>(a, [&](auto w, auto lpr, auto nv, auto al) { return run_fwd<IO, w.value, lpr.value, nv.value, al.value>(a, s); });
 }
 
 }  // namespace
