@@ -647,7 +647,8 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
 //   in_u = exp(b_u) dz_u . W q_u,  out_s = exp(b_C - b_s) e_s v_s . G k_s,  past = exp(b_C) <G, W>.
 // Only the row - col sums cancel, over one chunk; nothing grows with the sequence.  `past` follows
 // from <G, W> at the segment's end: past_c = <G, W>_end(c) - sum out, <G, W>_start(c) = past_c +
-// sum in.  The two kernels store row, in, col, out per token, and gl_dgate_kernel adds them.
+// sum in.  gl_dq_kernel leaves in_u and <G, W> at the segments' ends in the workspace, and
+// gl_dkv_kernel, which comes after it, adds the rest as it walks the chunks backward.
 template <typename IO, int D>
 struct DqLds {
   typedef Shape<IO, D> S;
@@ -674,8 +675,7 @@ __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
   const IO* dz = static_cast<const IO*>(a.dz) + s.row0 * D;
   IO* dq = static_cast<IO*>(a.dq) + s.row0 * D;
   const int nchunks = (T + kC - 1) / kC, first = seg * a.spc, end = min(nchunks, first + a.spc);
-  const size_t rows_all = static_cast<size_t>(a.B) * a.H * T;
-  float* in_o = a.ws_tok ? a.ws_tok + s.row0 + rows_all : nullptr;
+  float* in_o = a.ws_tok ? a.ws_tok + s.row0 : nullptr;
 
   // what a chunk's step needs in registers: its tiles, and the gates of the chunk after it
   struct Set {
@@ -814,20 +814,23 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
   IO* out = static_cast<IO*>(dk_group ? a.dk : a.dv) + s.row0 * D;
   float* de_o = a.deta_tok ? a.deta_tok + s.row0 : nullptr;
   const int nchunks = (T + kC - 1) / kC, first = seg * a.spc, end = min(nchunks, first + a.spc);
-  const size_t rows_all = static_cast<size_t>(a.B) * a.H * T;
-  float* col_o = a.ws_tok ? a.ws_tok + s.row0 + 2 * rows_all : nullptr;
-  float* out_o = a.ws_tok ? col_o + rows_all : nullptr;
-  float* row_o = a.ws_tok ? a.ws_tok + s.row0 : nullptr;
+  float* dg_o = a.dgate ? a.dgate + s.row0 : nullptr;
+  const float* in_i = a.dgate ? a.ws_tok + s.row0 : nullptr;
 
   // what a chunk's step needs in registers: its tiles, and the gates of the chunk before it
   struct Set {
     Tile<IO, D, 8 * D> q, k, v, z;
     GateRate gr;
   } y;
+  // what the per-token results of the chunk after it need: its in_u and gate
+  float in_u, gate_u;
   auto fetch = [&](int c, int tid) {
     const int lane = tid & 63;
     const long long c0 = static_cast<long long>(c) * kC;
     y.gr.load(s, c0 - kC, lane);
+    const int tokens = c >= first && dg_o ? min(kC, T - static_cast<int>(c0)) * 4 : 0;
+    in_u = GateRate::load1(gl_span(in_i + c0, tokens), lane);
+    gate_u = GateRate::load1(gl_span(s.gate + c0, tokens), lane);
     const int valid = c >= first ? s.len - static_cast<int>(c0) : 0;
     y.q.load(q, c0, valid, tid);
     y.k.load(k, c0, valid, tid);
@@ -835,31 +838,61 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
     y.z.load(dz, c0, valid, tid);
   };
   const bool decayer = wave == 2 * NW - 1;  // the wave that forms the next chunk's decays
-  // sums of a chunk whose shares are in LDS, stored by wave 0 (c >= end: nothing)
-  auto flush = [&](int c, const float* es, int lane) {
-    const int c0 = c * kC, bytes = wave == 0 && c < end ? min(kC, T - c0) * 4 : 0;
+  // The per-token results of a chunk, formed by one wave while the others work on the next chunk:
+  // the shares are read from LDS before that chunk's may overwrite them.
+  const bool teller = wave == (NW > 1 ? 2 * NW - 2 : 0);
+  struct Told {
+    float col, row, out, de, in, gate;
+  };
+  auto shares = [&](const float* es, float in, float gate, int lane) {
+    Told t;
     float o = 0.0f, col = 0.0f, row = 0.0f;
 #pragma unroll
     for (int i = 0; i < NW; ++i) o += L.part[i][lane];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      row += t <= lane >> 4 ? L.rows[t][lane] : 0.0f;
-      col += t >= lane >> 4 ? L.pairs[t][lane] : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      row += i <= lane >> 4 ? L.rows[i][lane] : 0.0f;
+      col += i >= lane >> 4 ? L.pairs[i][lane] : 0.0f;
     }
     const float e = es[lane];
-    store1(c0 + lane < s.len ? a.eta * (col + L.diag[lane] + o) : 0.0f, gl_span(de_o + c0, de_o ? bytes : 0), lane);
-    const int sums = a.ws_tok ? bytes : 0;
-    store1(e * col, gl_span(col_o + c0, sums), lane);
-    store1(e * o, gl_span(out_o + c0, sums), lane);
-    store1(row, gl_span(row_o + c0, sums), lane);
+    t.de = a.eta * (col + L.diag[lane] + o);
+    t.col = e * col;
+    t.out = e * o;
+    t.row = row;
+    t.in = in;
+    t.gate = gate;
+    return t;
+  };
+  double later = 0.0;  // <G, W> at the end of the chunk that is next to be told
+  if (dg_o && teller) {
+    const double* ends = a.ws_end + static_cast<size_t>(blockIdx.x) * NW;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) later += ends[i];
+  }
+  auto tell = [&](const Told& t, int c, int lane) {  // c >= end: nothing
+    const int c0 = c * kC, bytes = teller && c < end ? min(kC, T - c0) * 4 : 0;
+    float dg = 0.0f;
+    if (dg_o && teller && c < end) {
+      const double suf = gl_prefix(static_cast<double>(t.row) - t.col + t.in), pre = gl_prefix(static_cast<double>(t.out));
+      const double in = gl_prefix(static_cast<double>(t.in));
+      const double past = later - __shfl(pre, 63, 64);
+      const double from_here = __shfl(suf, 63, 64) - suf + (static_cast<double>(t.row) - t.col + t.in);
+      later = past + __shfl(in, 63, 64);
+      // a token that forgets everything (decay 0) takes no gradient
+      const bool live = c0 + lane < s.len && !(static_cast<double>(t.gate) * 1.4426950408889634 <= kGlNever);
+      dg = live ? static_cast<float>(from_here + (pre - t.out) + past) : 0.0f;
+    }
+    store1(c0 + lane < s.len ? t.de : 0.0f, gl_span(de_o + c0, de_o ? bytes : 0), lane);
+    store1(dg, gl_span(dg_o + c0, dg_o ? bytes : 0), lane);
   };
 
   gl_f4 x[NW];  // G's rows 16 wv + r (dv) or its columns (dk)
+  float last_in = 0.0f, last_gate = 0.0f;
   if (first < end) {
     GateRate gr;
     gr.load(s, static_cast<long long>(end - 1) * kC, lane);
     fetch(end - 1, tid);
-    no_store<8>();
+    no_store<6>();
     if (decayer) gr.decays(s, a.eta, static_cast<long long>(end - 1) * kC, &L.dec[0], lane);
   }
   if (dk_group) load_state<IO, D, false>(x, segment_state<D>(a, 1, chain, seg), wv, g, r);
@@ -874,13 +907,16 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
     const int c0 = c * kC, turn = (end - 1 - c) & 1;
     const GlDecays& dec = L.dec[turn];
     gl_barrier();  // the previous chunk's tiles have been read, its sums are whole
-    flush(c + 1, L.dec[turn ^ 1].e, lane);
+    const Told told = shares(L.dec[turn ^ 1].e, last_in, last_gate, lane);
+    last_in = in_u;
+    last_gate = gate_u;
     y.q.put(L.q, tid);
     y.k.put(L.k, tid);
     y.v.put(L.v, tid);
     y.z.put(L.z, tid);
     const GateRate gr = y.gr;
     gl_barrier();
+    tell(told, c + 1, lane);
     fetch(c - 1, tid);
     if (decayer && c > first) gr.decays(s, a.eta, static_cast<long long>(c - 1) * kC, &L.dec[turn ^ 1], lane);
     // rows s of P^T and R^T (decayed, without e_s)
@@ -960,59 +996,9 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
   }
   if (first < end) {
     gl_barrier();
-    flush(first, L.dec[(end - 1 - first) & 1].e, lane);
+    tell(shares(L.dec[(end - 1 - first) & 1].e, last_in, last_gate, lane), first, lane);
   }
   if (seg == 0 && !dk_group) store_state_transposed<IO, D>(x, a.dw0 + static_cast<size_t>(chain) * D * D, wv, g, r);
-}
-
-// dlog_gate from the per-token sums (see above): a workgroup per segment, a wave per chunk, lane =
-// token.  First every chunk's sum of in - out, then for each chunk the sums of the later ones.
-constexpr int kGateWaves = 8;
-__global__ __launch_bounds__(64 * kGateWaves) void gl_dgate_kernel(GatedArgs a, int nend) {
-  extern __shared__ double chunk_sum[];  // [spc]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int nchunks = (a.T + kC - 1) / kC;
-  const int chain = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
-  const int first = seg * a.spc, n = min(a.spc, nchunks - first);
-  const size_t all = static_cast<size_t>(a.B) * a.H * a.T, row0 = static_cast<size_t>(chain) * a.T;
-  const float* row = a.ws_tok + row0;
-  const float* in = row + all;
-  const float* col = in + all;
-  const float* out = col + all;
-  const int len = gl_length(a.lengths, chain / a.H, a.T);
-  auto wave_sum = [](double x) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
-    return x;
-  };
-  for (int c = wave; c < n; c += kGateWaves) {
-    const int t = (first + c) * kC + lane;
-    const double x = wave_sum(t < a.T ? static_cast<double>(in[t]) - out[t] : 0.0);
-    if (lane == 0) chunk_sum[c] = x;
-  }
-  __syncthreads();
-  for (int c = wave; c < n; c += kGateWaves) {
-    // over the later chunks, and <G, W> at the segment's end
-    double later = lane < nend ? a.ws_end[static_cast<size_t>(blockIdx.x) * nend + lane] : 0.0;
-    for (int i = c + 1 + lane; i < n; i += 64) later += chunk_sum[i];
-    later = wave_sum(later);
-    const int t = (first + c) * kC + lane;
-    const bool have = t < a.T;
-    double suf = have ? static_cast<double>(row[t]) - col[t] + in[t] : 0.0;  // over u >= t
-    const double o_t = have ? static_cast<double>(out[t]) : 0.0;
-    double pre = o_t;  // over s <= t
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double x = __shfl_down(suf, o, 64), y = __shfl_up(pre, o, 64);
-      if (lane + o < 64) suf += x;
-      if (lane >= o) pre += y;
-    }
-    const double past = later - __shfl(pre, 63, 64);
-    if (!have) continue;
-    // a token that forgets everything (decay 0) takes no gradient
-    const bool live = t < len && !(static_cast<double>(a.gate[row0 + t]) * 1.4426950408889634 <= kGlNever);
-    a.dgate[row0 + t] = live ? static_cast<float>(suf + (pre - o_t) + past) : 0.0f;
-  }
 }
 
 // ---------------------------------------------------------------- host
@@ -1088,15 +1074,10 @@ hipError_t bwd(const GatedArgs& a, hipStream_t s) {
   if (a.T > 0) dq<<<dim3(groups), dim3(4 * D), dq_bytes, s>>>(a);
   dkv<<<dim3(groups), dim3(8 * D), dkv_bytes, s>>>(a);
   e = hipGetLastError();
-  if (e != hipSuccess || !a.dgate || a.T == 0) return e;
-  const int sums = a.spc * static_cast<int>(sizeof(double));
-  e = allow_lds(gl_dgate_kernel, sums);
-  if (e != hipSuccess) return e;
-  gl_dgate_kernel<<<dim3(groups), dim3(64 * kGateWaves), sums, s>>>(a, D / 16);
-  return hipGetLastError();
+  return e;
 }
 
-// The workspace: [ends, doubles][state sums][gradient sums][decays][per-token sums], each part
+// The workspace: [ends, doubles][state sums][gradient sums][decays][in_u per token], each part
 // only where the call needs it; every part but the last is a multiple of 16 bytes.
 size_t carve(GatedArgs* a, int d, bool bwd, bool gated, void* ws) {
   plan(a, bwd);
@@ -1114,7 +1095,7 @@ size_t carve(GatedArgs* a, int d, bool bwd, bool gated, void* ws) {
     if (bwd) a->seg_g = reinterpret_cast<float*>(take(segs * dd * sizeof(float)));
     a->seg_decay = reinterpret_cast<float*>(take(2 * segs * sizeof(float)));
   }
-  if (gated) a->ws_tok = reinterpret_cast<float*>(take(static_cast<size_t>(a->B) * a->H * a->T * 4 * sizeof(float)));
+  if (gated) a->ws_tok = reinterpret_cast<float*>(take(static_cast<size_t>(a->B) * a->H * a->T * sizeof(float)));
   return at;
 }
 

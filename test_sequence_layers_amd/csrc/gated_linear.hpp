@@ -50,17 +50,23 @@ __device__ __forceinline__ double gl_dpp(double x) {
   return __builtin_bit_cast(double, pair{lo, hi});
 }
 
-// One wave, lane = token: g is the token's log decay (0 past the sequence).  The prefix sum
-// runs in 64 bits: b_u - b_s is a small difference of sums that may be large.
-__device__ __forceinline__ void gl_decays(float g, float e, GlDecays* d, int lane) {
-  double x = static_cast<double>(g) * 1.4426950408889634;
-  if (x < kGlNever) x = kGlNever;  // a NaN stays one
+// sum over the lanes up to and with this one
+__device__ __forceinline__ double gl_prefix(double x) {
   x += gl_dpp<0x111, 0xF>(x);  // row_shr 1, 2, 4, 8: sums of 16 lanes
   x += gl_dpp<0x112, 0xF>(x);
   x += gl_dpp<0x114, 0xF>(x);
   x += gl_dpp<0x118, 0xF>(x);
   x += gl_dpp<0x142, 0xA>(x);  // row_bcast 15 into rows 1 and 3, row_bcast 31 into rows 2 and 3
   x += gl_dpp<0x143, 0xC>(x);
+  return x;
+}
+
+// One wave, lane = token: g is the token's log decay (0 past the sequence).  The prefix sum
+// runs in 64 bits: b_u - b_s is a small difference of sums that may be large.
+__device__ __forceinline__ void gl_decays(float g, float e, GlDecays* d, int lane) {
+  double x = static_cast<double>(g) * 1.4426950408889634;
+  if (x < kGlNever) x = kGlNever;  // a NaN stays one
+  x = gl_prefix(x);
   const double last = __shfl(x, kGlChunk - 1, 64);
   const float h = static_cast<float>(x), to = __builtin_amdgcn_exp2f(static_cast<float>(last - x));
   d->bh[lane] = h;
