@@ -602,7 +602,11 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
         const float uh = dec.bh[u], ul = dec.bl[u];
         const gl_f4 sh = at4(dec.bh, s4), sl = at4(dec.bl, s4), e = at4(dec.e, s4);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) p[i][x] = s4 + x <= u ? p[i][x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
+        for (int x = 0; x < 4; ++x) p[i][x] *= gl_between(uh, ul, sh[x], sl[x]) * e[x];
+        if (ut[i] == st[i]) {  // the diagonal: pairs s <= u only
+#pragma unroll
+          for (int x = 0; x < 4; ++x) p[i][x] = s4 + x <= u ? p[i][x] : 0.0f;
+        }
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) M::put(factor_row<IO>(L.p, ut[i], r), st[i], g, p[i]);
@@ -694,8 +698,10 @@ __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
   // in_u of a chunk whose shares are in LDS, stored by wave 0 (c < first: nothing)
   auto flush = [&](int c) {
     float in = 0.0f;
+    if (wv == 0) {
 #pragma unroll
-    for (int x = 0; x < NW; ++x) in += L.part[x][lane];
+      for (int x = 0; x < NW; ++x) in += L.part[x][lane];
+    }
     store1(in, gl_span(in_o + c * kC, in_o && wv == 0 && c >= first ? min(kC, T - c * kC) * 4 : 0), lane);
   };
 
@@ -741,7 +747,11 @@ __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
         const float uh = dec.bh[u], ul = dec.bl[u];
         const gl_f4 sh = at4(dec.bh, s4), sl = at4(dec.bl, s4), e = at4(dec.e, s4);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) rd[i][x] = s4 + x <= u ? rd[i][x] * (gl_between(uh, ul, sh[x], sl[x]) * e[x]) : 0.0f;
+        for (int x = 0; x < 4; ++x) rd[i][x] *= gl_between(uh, ul, sh[x], sl[x]) * e[x];
+        if (ut[i] == st[i]) {  // the diagonal: pairs s <= u only
+#pragma unroll
+          for (int x = 0; x < 4; ++x) rd[i][x] = s4 + x <= u ? rd[i][x] : 0.0f;
+        }
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) M::put(factor_row<IO>(L.r, ut[i], r), st[i], g, rd[i]);
@@ -845,7 +855,8 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
     float col, row, out, de, in, gate;
   };
   auto shares = [&](const float* es, float in, float gate, int lane) {
-    Told t;
+    Told t = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (!teller) return t;
     float o = 0.0f, col = 0.0f, row = 0.0f;
 #pragma unroll
     for (int i = 0; i < NW; ++i) o += L.part[i][lane];
@@ -938,15 +949,27 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
         const gl_f4 uh = at4(dec.bh, u4), ul = at4(dec.bl, u4);
         float cs = 0.0f, dg = 0.0f;
         gl_f4 rows;
+        if (ut[i] != st[i]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float f = gl_between(uh[j], ul[j], sh, sl);
-          const float m = p[i][j] * rd[i][j] * f, below = u4 + j > ss ? m : 0.0f;
-          p[i][j] = u4 + j >= ss ? p[i][j] * f : 0.0f;
-          rd[i][j] = u4 + j >= ss ? rd[i][j] * f : 0.0f;
-          cs += below;
-          dg += u4 + j == ss ? m : 0.0f;
-          rows[j] = below * es;
+          for (int j = 0; j < 4; ++j) {
+            const float f = gl_between(uh[j], ul[j], sh, sl);
+            p[i][j] *= f;
+            const float m = p[i][j] * rd[i][j];
+            rd[i][j] *= f;
+            cs += m;
+            rows[j] = m * es;
+          }
+        } else {  // the diagonal: pairs u >= s only
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float f = gl_between(uh[j], ul[j], sh, sl);
+            const float m = p[i][j] * rd[i][j] * f, below = u4 + j > ss ? m : 0.0f;
+            p[i][j] = u4 + j >= ss ? p[i][j] * f : 0.0f;
+            rd[i][j] = u4 + j >= ss ? rd[i][j] * f : 0.0f;
+            cs += below;
+            dg += u4 + j == ss ? m : 0.0f;
+            rows[j] = below * es;
+          }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) rows[j] = over_r(rows[j]);
