@@ -224,6 +224,55 @@ def time_backward(w, steps, warmup, torch, ttt, rates=False):
     return {"ms_per_step": ms, "tokens_per_s": w.B * w.T / (ms * 1e-3)}
 
 
+def time_neighbours(steps, torch, ttt):
+    """The layers' neighbours at the headline shape (B = 8, H = 12, T = 2048, d = 64, bf16): the gated
+    linear recurrence (forward, backward; one token of 512 sequences) and the norm after a layer with
+    gate and residual (forward, backward).  Seeded inputs, rotated over sets that exceed the 256 MB
+    Infinity Cache.  ms per call, and the bytes that cannot be avoided over it."""
+    B, H, T, d = 8, 12, 2048, 64
+    gen = torch.Generator(device="cuda").manual_seed(2000)
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    tok = lambda: normal(B, H, T, d).to(torch.bfloat16)
+    gate = lambda: torch.nn.functional.logsigmoid(normal(B, H, T) + 4.0)
+    sets = []
+    for _ in range(4):
+        k = normal(B, H, T, d)
+        sets.append({"q": tok(), "k": (k / k.norm(dim=-1, keepdim=True)).to(torch.bfloat16), "v": tok(),
+                     "dz": tok(), "g": gate(), "rate": torch.rand((B, H, T), generator=gen, device="cuda")})
+    w0, scale = 0.02 * normal(H, d, d), normal(H, d)
+    step = [(normal(512, H, d).to(torch.bfloat16), normal(512, H, d, d)) for _ in range(3)]
+    n, s = B * H * T * d * 2, B * H * d * d * 4
+    per_token = B * H * T * 8
+    calls = {
+        "gated_linear_d64_T2048": (len(sets), 4 * n + per_token + s // B + s, lambda i: ttt.gated_linear_fwd(
+            sets[i]["q"], sets[i]["k"], sets[i]["v"], w0, 0.5, sets[i]["g"], eta_tok=sets[i]["rate"], return_state=True)),
+        "gated_linear_d64_T2048+backward": (len(sets), 7 * n + 2 * per_token + s // B + s, lambda i: ttt.gated_linear_bwd(
+            sets[i]["q"], sets[i]["k"], sets[i]["v"], w0, 0.5, sets[i]["g"], sets[i]["dz"], eta_tok=sets[i]["rate"])),
+        "gated_linear_step_B512": (len(step), 2 * 512 * H * d * d * 4 + 4 * 512 * H * d * 2, lambda i: ttt.gated_linear_step(
+            step[i][0], step[i][0], step[i][0], step[i][1], 0.01, None)),
+        "token_norm_d64_T2048": (len(sets), 4 * n, lambda i: ttt.token_norm_fwd(
+            sets[i]["q"], "rms", 1e-5, weight=scale, gate=sets[i]["k"], scale=scale, res=sets[i]["v"])),
+        "token_norm_d64_T2048+backward": (len(sets), 5 * n, lambda i: ttt.token_norm_bwd(
+            sets[i]["q"], sets[i]["dz"], "rms", 1e-5, weight=scale, gate=sets[i]["k"], scale=scale)),
+    }
+    out = {}
+    for name, (count, nbytes, call) in calls.items():
+        for i in range(5):
+            call(i % count)
+        torch.cuda.synchronize()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for i in range(steps):
+            call(i % count)
+        b.record()
+        torch.cuda.synchronize()
+        ms = a.elapsed_time(b) / steps
+        tokens = 512 if "step" in name else B * T
+        out[name] = {"tokens_per_s": round(tokens / ms * 1e3, 1), "ms_per_step": round(ms, 5),
+                     "hbm_gbs": round(nbytes / ms / 1e6, 1)}
+    return out
+
+
 def _cpu_model():
     try:
         with open("/proc/cpuinfo") as f:
@@ -492,6 +541,7 @@ def main():
                 "tflops": round(r["tflops"], 3),
                 "mfma_util_pct": round(100 * r["tflops"] / BF16_MFMA_PEAK_TFLOPS, 3),
             }
+        others.update(time_neighbours(max(10, args.steps // 2), torch, ttt))
         line["other_workloads"] = others
     if not args.no_cpu:
         line["cpu_baseline"] = cpu_baseline(w)

@@ -6,6 +6,12 @@
 // that into the state at each segment's start, and the main kernel walks the segments' chunks.
 // The d x d state stays in registers, 16 columns a wave, in the MFMA C layout.
 //
+// Why segments: a chunk of 64 tokens takes one workgroup 2.6 us (d = 64, bf16) however many run, so
+// 96 sequences of 2048 tokens, one workgroup each, took 190 us with the chip two thirds idle;
+// reading K and V once more for the segments' sums (15 us) and the scan (6 us) let the rest take
+// 27 us (3.8 TB/s).  Chunks of 64: the products inside a chunk grow with it, the state's splits
+// and its 24 products a wave are paid once for it.
+//
 // Every product is a sum of 16 x 16 tiles C = A B.  Lane (g, r) of a wave holds row r of A and
 // column r of B at eight k of each block of 32, the same ones for both, and rows 4 g + e (e =
 // 0..3) of column r of C.  So two C tiles are an operand whose k runs along their rows, with no
@@ -14,7 +20,9 @@
 //   float32 I/O:  v_mfma_f32_16x16x4_f32.
 //   bf16 I/O:     v_mfma_f32_16x16x32_bf16.  Products of inputs are exact.  Factors that are not
 //     inputs are split into bf16 parts, x = hi + mid + lo: two parts (2^-16 of a term) where the
-//     result is rounded to bf16, three (2^-24) where it is a float32 output or the state itself.
+//     result is rounded to bf16, three (2^-24) where it is a float32 output or the state itself
+//     (with two, final states were off by 2.4e-6 and gate gradients by 3.8e-6; with three by
+//     7e-8 and 1.8e-7).
 #include <type_traits>
 
 #include "gated_linear.hpp"
@@ -412,6 +420,8 @@ __device__ __forceinline__ gl_f4 row_products(const typename Math<IO>::Elem* a, 
 // What a segment adds to the state from zero.  Side 0: sum over its tokens s of (decay to the
 // segment's end) e_s v_s k_s^T, for the states.  Side 1 (backward): sum over its tokens u of
 // (decay from the segment's start) dz_u q_u^T, for the states' gradients.
+// Bound by the loads' latency: 768 workgroups of 4 chunks read K and V of 8 x 12 x 2048 tokens (d = 64,
+// bf16) in 15 us, 2.9 TB/s of them.
 template <typename IO, int D>
 struct SumsLds {
   typename Math<IO>::Elem a[Shape<IO, D>::kTile], b[Shape<IO, D>::kTile];
@@ -480,7 +490,8 @@ __global__ __launch_bounds__(4 * D) void gl_sums_kernel(GatedArgs a) {
 
 // The sums become the states at the segments' starts (side 0, first to last from w0) and the
 // gradients at their ends (side 1, last to first from dw_out), in place.
-// VEC elements a thread; the sums of kAhead segments are loaded before the first is used.
+// VEC elements a thread; the sums of kAhead segments are loaded before the first is used (one
+// after another took 22 us on 16 sequences of 43 segments, eight at a time 9 us).
 template <int D, int VEC>
 __global__ __launch_bounds__(256) void gl_scan_kernel(GatedArgs a) {
   typedef float vec __attribute__((ext_vector_type(VEC)));
@@ -526,6 +537,12 @@ __device__ __forceinline__ const float* segment_state(const GatedArgs& a, int si
 }
 
 // ---------------------------------------------------------------- forward
+//
+// Three barriers a chunk: tiles free, tiles staged (the next ones' loads start here), P ready.  The
+// next chunk's decays are formed by one wave while the others form P.  P's ten blocks of 16 x 16
+// pairs are dealt to the waves, the rest splits by output features: V, the state and its update
+// need no exchange.  Bound by HBM while three workgroups share a CU: 61 us on 16 sequences of 32749
+// tokens (d = 64, bf16), 4.4 TB/s of q, k, v and z.
 template <typename IO, int D>
 struct FwdLds {
   typename Math<IO>::Elem q[Shape<IO, D>::kTile], k[Shape<IO, D>::kTile], v[Shape<IO, D>::kTile];
@@ -653,6 +670,12 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
 // from <G, W> at the segment's end: past_c = <G, W>_end(c) - sum out, <G, W>_start(c) = past_c +
 // sum in.  gl_dq_kernel leaves in_u and <G, W> at the segments' ends in the workspace, and
 // gl_dkv_kernel, which comes after it, adds the rest as it walks the chunks backward.
+//
+// Two kernels rather than one with two kinds of workgroups: dk and dv want eight waves (each
+// half keeps one orientation of G: as four waves with both, 114 us for all gradients of 8 x 12 x
+// 2048 tokens, d = 64, bf16; as two kernels 42 + 56).  dq then needs no Q in LDS and three of its
+// workgroups fit a CU.  42 us is 3.0 TB/s of its five tensors; the factors' parts and the products of
+// two parts more than the forward pass, on three waves a SIMD, keep it from HBM's rate.
 template <typename IO, int D>
 struct DqLds {
   typedef Shape<IO, D> S;
@@ -792,7 +815,9 @@ __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
   }
 }
 
-// Two waves for each 16 columns: one group has G^T's columns for dv, the other G's for dk.
+// Two waves for each 16 columns: one group has G^T's columns for dv, the other G's for dk.  Bound by
+// the vector units (60 % of its time: splits, decays, the pairs' sums): 56 us at the size above, 2.7
+// TB/s of its six tensors.
 template <typename IO, int D>
 struct DkvLds {
   typedef Shape<IO, D> S;
@@ -1027,7 +1052,12 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
 // ---------------------------------------------------------------- host
 
 // Chunks per segment: the number of segments that takes the fewest rounds of chunks, where `slots`
-// workgroups run at once and each spends about kStart chunks' time before its first.
+// workgroups run at once (forward three a CU, backward two) and each spends about kStart chunks'
+// time before its first.  All kernels of a call, d = 64, bf16, at 256, 512, 768, 1024 and 1536 slots:
+//   forward, 96 sequences of 32 chunks: 65, 49, 47, 48, 56 us; 16 of 512: 126, 105, 107, 113, 123;
+//   backward, 96 of 32: 151, 130, 133, 133, 156; 64 of 128: 318, 299, 312, 313, 346.
+// `launches`: what the two further launches cost, in chunks: 12 sequences of 256 tokens take 15 us
+// in one segment and 22 us in four, of 512 tokens the same 22 us.
 void plan(GatedArgs* a, bool bwd) {
   constexpr int kStart = 2;
   const int launches = bwd ? 1 : 3;  // chunks' time that the two more launches take

@@ -105,7 +105,7 @@ def test_refusals(lib, fn, bad, want):
 @pytest.mark.parametrize("fn", ALL[:2])
 @pytest.mark.parametrize("bad, want", [
     (dict(T=-1), INVALID), (dict(stride=-4), INVALID), (dict(stride=3), INVALID), (dict(lengths=FAKE + 2), INVALID),
-    (dict(B=1 << 15, H=1 << 14, T=1 << 20), UNSUPPORTED)])
+    (dict(B=1 << 15, H=1 << 14, T=1 << 20), UNSUPPORTED), (dict(T=(1 << 30) + 1), UNSUPPORTED)])
 def test_refusals_of_sequences(lib, fn, bad, want):
     assert _call(lib, fn, **bad) == want
     assert fn in ttt.last_error()
@@ -204,6 +204,112 @@ def test_ragged_batch(io, d):
         assert_within(n, t, ref[n], tol[n])
     for n in ("z", "dq", "dk", "dv", "dlog_gate", "deta_tok"):
         assert not got[n][0].any() and not got[n][1, :, 1:].any(), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [40, 700])
+def test_rates_without_a_gate(io, T):
+    _check(gated_inputs(2, 2, T, 64, io, "none", rates=True, seed=23))
+
+
+@pytest.mark.gpu
+def test_given_outputs_are_written_whole():
+    x = _to_gpu(gated_inputs(2, 3, 150, 32, "bf16", "soft", lengths=[70, 150], seed=24))
+    z, w = torch.full_like(x["q"], 7.0), torch.full((2, 3, 32, 32), 7.0, device="cuda")
+    got = _forward(x, z=z, w_out=w)
+    assert got[0] is z and got[1] is w and not z[0, :, 70:].any()
+    want = _forward(x)
+    assert torch.equal(z, want[0]) and torch.equal(w, want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_callers_workspace(io):
+    """A workspace of exactly the size asked for, whatever it holds, and one byte less."""
+    x = _to_gpu(gated_inputs(2, 3, 1500, 64, io, "resets", rates=True, seed=25))
+    dt = x["q"].dtype
+    sizes = (ttt.gated_linear_fwd_workspace_size(2, 3, 1500, 64, dt),
+             ttt.gated_linear_bwd_workspace_size(2, 3, 1500, 64, True, dt))
+    assert min(sizes) > 0 and ttt.gated_linear_bwd_workspace_size(2, 3, 1500, 64, False, dt) < sizes[1]
+    want = (*_forward(x), *_backward(x).values())
+    for fill in (0, 255):
+        ws = [torch.full((n + 64,), fill, dtype=torch.uint8, device="cuda") for n in sizes]
+        got = (*_forward(x, workspace=ws[0][:sizes[0]]), *_backward(x, workspace=ws[1][:sizes[1]]).values())
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        for w, n in zip(ws, sizes):
+            assert (w[n:] == fill).all()  # nothing behind it is written
+    for call, n in ((_forward, sizes[0]), (_backward, sizes[1])):
+        with pytest.raises(ttt.TTTError, match="workspace"):
+            call(x, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.gpu
+def test_two_graphs_share_a_workspace():
+    xs = [_to_gpu(gated_inputs(2, 3, 900, 64, "bf16", "soft", rates=True, seed=s)) for s in (26, 27)]
+    want = [(*_forward(x), *_backward(x).values()) for x in xs]
+    ws = torch.empty(max(ttt.gated_linear_fwd_workspace_size(2, 3, 900, 64, torch.bfloat16),
+                         ttt.gated_linear_bwd_workspace_size(2, 3, 900, 64, True, torch.bfloat16)),
+                     dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((*_forward(x, workspace=ws), *_backward(x, workspace=ws).values()))
+        graphs.append(g)
+    for i in (0, 1, 1, 0):
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[i], outs[i]))
+        assert torch.equal(_forward(xs[i])[0], want[i][0])  # the program's own work between replays
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Heads whose elements lie 2^32 behind the tensor's start; the last documents are checked."""
+    H, T, d = 5, (1 << 24) + 192, 64
+    gen = torch.Generator("cuda").manual_seed(28)
+    x = torch.randn((1, H, T, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    assert x.numel() > 1 << 32
+    g = torch.full((1, H, T), -0.05, device="cuda")
+    g[..., T - 150] = -float("inf")
+    w0 = torch.zeros((H, d, d), device="cuda")
+    z, w = ttt.gated_linear_fwd(x, x, x, w0, 0.01, g, return_state=True)
+    tail = x[:, :, T - 150:].cpu()
+    small = {"q": tail, "k": tail, "v": tail, "dz": tail, "w0": w0.cpu(), "dw_out": torch.zeros(1, H, d, d),
+             "log_gate": g[:, :, T - 150:].cpu(), "eta_tok": None, "lengths": None, "eta": 0.01}
+    ref = gated_reference(small, backward=False)
+    # the tail's chunks begin elsewhere in the long sequence: one more state's product and sum
+    tol = gated_bounds({**small, "log_gate": small["log_gate"]}, ref, backward=False)
+    assert_within("z", z[:, :, T - 150:], ref["z"], 1.1 * tol["z"])
+    assert_within("w_out", w, ref["w_out"], 1.1 * tol["w_out"])
+
+
+@pytest.mark.gpu
+def test_short_row_of_a_very_long_padded_batch():
+    """A row of 70 tokens padded to more than 2^24: nothing is read past it."""
+    T, d = (1 << 24) + 4096, 64
+    x = gated_inputs(1, 1, 128, d, "bf16", "soft", rates=True, lengths=[70], seed=29)
+    ref = gated_reference(x)
+    tol = gated_bounds(x, ref)
+    g = _to_gpu(x)
+    for n in ("q", "k", "v", "dz"):
+        big = torch.full((1, 1, T, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+        big[:, :, :128] = g[n]
+        g[n] = big
+    for n in ("log_gate", "eta_tok"):
+        big = torch.full((1, 1, T), float("nan"), device="cuda")
+        big[:, :, :128] = g[n]
+        g[n] = big
+    z, w = _forward(g)
+    got = {"z": z, "w_out": w, **_backward(g)}
+    for n, t in got.items():
+        if n in ("w_out", "dw0"):
+            assert_within(n, t, ref[n], tol[n])
+        else:
+            assert_within(n, t[:, :, :128], ref[n], tol[n])
+            assert not t[:, :, 128:].any(), n
 
 
 @pytest.mark.gpu

@@ -139,6 +139,46 @@ def test_rows_without_spread(kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 65, 600])
+def test_a_row_that_is_not_finite_stays_by_itself(d):
+    p, dy = _inputs(1, 2, 40, d, "bf16", seed=12)
+    g = _gpu(p)
+    want, grads = _fwd(g, "layer", "silu", 1e-5), _bwd(g, dy.cuda(), "layer", "silu", 1e-5)
+    bad = {**g, "x": g["x"].clone()}
+    bad["x"][0, 1, 7, 3] = float("inf")
+    keep = torch.ones(1, 2, 40, dtype=torch.bool, device="cuda")
+    keep[0, 1, 7] = False
+    y, got = _fwd(bad, "layer", "silu", 1e-5), _bwd(bad, dy.cuda(), "layer", "silu", 1e-5)
+    assert not torch.isfinite(y[0, 1, 7].float()).all()
+    for a, b in ((want, y), (grads["dx"], got["dx"]), (grads["dgate"], got["dgate"])):
+        assert torch.equal(a[keep], b[keep])
+    assert torch.equal(grads["dweight"][0], got["dweight"][0])  # the other head's sums
+
+
+@pytest.mark.gpu
+def test_more_than_2_to_32_elements():
+    B, H, T, d = 1, 3, 90_000, 16_000
+    gen = torch.Generator("cuda").manual_seed(13)
+    x = torch.randn((B, H, T, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    assert x.numel() > 1 << 32
+    w = torch.randn((H, d), generator=gen, device="cuda")
+    y = ttt.token_norm_fwd(x, "rms", 1e-5, weight=w)
+    dx, dw, _, _, _ = ttt.token_norm_bwd(x, x, "rms", 1e-5, weight=w)
+    tail = {"x": x[:, 2:, -4:].cpu(), "weight": w[2:].cpu()}
+    ref = norm_reference(tail, "rms", "none", 1e-5)
+    assert_within("y", y[:, 2:, -4:], ref, norm_bounds(tail, "rms", "none", 1e-5, ref_y=ref))
+    grads = norm_reference(tail, "rms", "none", 1e-5, tail["x"])
+    tol = norm_bounds(tail, "rms", "none", 1e-5, dy=tail["x"], ref=grads)
+    assert_within("dx", dx[:, 2:, -4:], grads["dx"], tol["dx"])
+    # sum over rows of x xh, with xh = x r: every term is positive, so 512 roundings bound the sum's error
+    part = torch.zeros(H, d, dtype=torch.float64, device="cuda")
+    for t in range(0, T, 5000):
+        xs = x[0, :, t:t + 5000].double()
+        part += (xs * xs * torch.rsqrt(xs.square().mean(-1, keepdim=True) + 1e-5)).sum(1)
+    assert float(((dw.double() - part) / part).abs().max()) < 1000 * 2.0 ** -24
+
+
+@pytest.mark.gpu
 def test_no_tokens():
     p, dy = _inputs(2, 3, 0, 64, "bf16", seed=7)
     g = _gpu(p)
