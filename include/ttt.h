@@ -364,9 +364,10 @@ int ttt_mlp_nc_bwd(const void* q, const void* k, const void* v,
  *              gate of -inf at each one's first token.
  *   lengths    int32 [B] device pointer or NULL: batch row b has min(max(lengths[b], 0), T)
  *              tokens.  Tokens past them are not read; their outputs and gradients are 0.
- *   q, k, v of tokens within the lengths are finite; a token that is not may make any output
+ *   q, k, v, dz of tokens within the lengths are finite; a token that is not may make any output
  *   of its sequence non-finite (forward up to a gate of -inf in a later block of 64 tokens).
- * d in {16, 32, 64}, both dtypes, 0 <= T <= 2^30 (T = 0: w_out receives the initial state).  Token
+ * d in {16, 32, 64}, both dtypes, 0 <= T <= 2^30 (T = 0: w_out receives the initial state), B*H*d
+ * < 2^29, B*H*(T/64 + 1) < 2^31 (more is TTT_E_UNSUPPORTED).  Token
  * tensors, states, their gradients and the workspace are 16-byte aligned, w0_batch_stride is
  * a multiple of 4 (TTT_E_INVALID otherwise); eta_tok, log_gate and lengths 4-byte aligned.
  * The states and every sum are float32; bf16 inputs are multiplied exactly.

@@ -328,7 +328,7 @@ struct GateRate {
     rate = load1(gl_span(s.rate + c0, s.rate ? bytes : 0), lane);
   }
   __device__ __forceinline__ void decays(const Seq& s, float eta, long long c0, GlDecays* d, int lane) const {
-    gl_decays(g, c0 >= 0 && c0 + lane < s.len ? (s.rate ? eta * rate : eta) : 0.0f, d, lane);
+    gl_decays(g, s.rate ? eta * rate : eta, c0 >= 0 && c0 + lane < s.len, d, lane);
   }
   static __device__ __forceinline__ float load1(__amdgpu_buffer_rsrc_t src, int i) {
     return __builtin_bit_cast(float, static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b32(src, i * 4, 0, 0)));
@@ -915,7 +915,7 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
       const double from_here = __shfl(suf, 63, 64) - suf + (static_cast<double>(t.row) - t.col + t.in);
       later = past + __shfl(in, 63, 64);
       // a token that forgets everything (decay 0) takes no gradient
-      const bool live = c0 + lane < s.len && !(static_cast<double>(t.gate) * 1.4426950408889634 <= kGlNever);
+      const bool live = c0 + lane < s.len && __builtin_amdgcn_exp2f(t.gate * 1.44269504f) != 0.0f;
       dg = live ? static_cast<float>(from_here + (pre - t.out) + past) : 0.0f;
     }
     store1(c0 + lane < s.len ? t.de : 0.0f, gl_span(de_o + c0, de_o ? bytes : 0), lane);

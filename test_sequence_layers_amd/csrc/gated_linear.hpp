@@ -19,8 +19,8 @@ constexpr int kGlPitch = kGlChunk + 4;   // row pitch (floats) of matrices with 
 struct GlDecays {
   float bh[kGlChunk], bl[kGlChunk];  // b_u / ln 2 as the sum of two floats
   float e[kGlChunk];                 // e_s (0 past the sequence)
-  float from[kGlChunk];              // exp(b_u): from the chunk's start
-  float to[kGlChunk];                // exp(b_C - b_s): to the chunk's end
+  float from[kGlChunk];              // exp(b_u): from the chunk's start (0 past the sequence)
+  float to[kGlChunk];                // exp(b_C - b_s): to the chunk's end (0 past the sequence)
   float to_e[kGlChunk];              // the same times e_s
   float whole[4];                    // exp(b_C) (first entry)
 };
@@ -61,18 +61,20 @@ __device__ __forceinline__ double gl_prefix(double x) {
   return x;
 }
 
-// One wave, lane = token: g is the token's log decay (0 past the sequence).  The prefix sum
-// runs in 64 bits: b_u - b_s is a small difference of sums that may be large.
-__device__ __forceinline__ void gl_decays(float g, float e, GlDecays* d, int lane) {
+// One wave, lane = token: g is the token's log decay (0 past the sequence), `live` whether it is
+// one of the sequence's: no state reaches the others, whatever it holds.  The prefix sum runs in 64
+// bits: b_u - b_s is a small difference of sums that may be large.
+__device__ __forceinline__ void gl_decays(float g, float e, bool live, GlDecays* d, int lane) {
   double x = static_cast<double>(g) * 1.4426950408889634;
   if (x < kGlNever) x = kGlNever;  // a NaN stays one
   x = gl_prefix(x);
   const double last = __shfl(x, kGlChunk - 1, 64);
-  const float h = static_cast<float>(x), to = __builtin_amdgcn_exp2f(static_cast<float>(last - x));
+  const float h = static_cast<float>(x), to = live ? __builtin_amdgcn_exp2f(static_cast<float>(last - x)) : 0.0f;
+  e = live ? e : 0.0f;
   d->bh[lane] = h;
   d->bl[lane] = static_cast<float>(x - h);
   d->e[lane] = e;
-  d->from[lane] = __builtin_amdgcn_exp2f(h);
+  d->from[lane] = live ? __builtin_amdgcn_exp2f(h) : 0.0f;
   d->to[lane] = to;
   d->to_e[lane] = to * e;
   if (lane == 0) d->whole[0] = __builtin_amdgcn_exp2f(static_cast<float>(last));

@@ -476,7 +476,8 @@ hipError_t run_fwd(const NormArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.B) * a.H * a.T;
   const long long groups = (rows + RB - 1) / RB;
   // several passes share a workgroup's start once there are workgroups enough
-  const int passes = groups >= 8192 ? 4 : groups >= 4096 ? 2 : 1;
+  // (and a grid holds less than 2^32 threads: at most 2^21 workgroups of 1024)
+  const int passes = groups >= 8192 ? static_cast<int>(groups >> 21) + 4 : groups >= 4096 ? 2 : 1;
   norm_fwd_kernel<IO, W, LPR, NV, A><<<dim3(static_cast<unsigned>((groups + passes - 1) / passes)), dim3(Block<LPR>::kThreads), 0, s>>>(
       a, static_cast<int>(rows), passes);
   return hipGetLastError();

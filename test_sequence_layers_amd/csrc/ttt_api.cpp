@@ -443,8 +443,10 @@ int check_gated(const char* fn, std::initializer_list<const void*> tokens,
     return fail(TTT_E_UNSUPPORTED, "%s: d=%d not supported (16, 32, 64)", fn, d);
   if (static_cast<long long>(B) * H > 0x3fffffffLL || !fits_int64(B, H, T > 0 ? T : 1, 4LL * d * d))
     return fail(TTT_E_INVALID, "%s: B*H*T*d overflows", fn);
-  if (T > (1 << 30) || static_cast<long long>(B) * H * (T / 64 + 1LL) > 0x7fffffffLL)
-    return fail(TTT_E_UNSUPPORTED, "%s: T > 2^30, or B*H*T/64 exceeds the grid limit", fn);
+  // a grid holds less than 2^32 threads: 8 d of them a sequence at most (all of step's at once)
+  if (T > (1 << 30) || static_cast<long long>(B) * H * (T / 64 + 1LL) > 0x7fffffffLL ||
+      static_cast<long long>(B) * H * d > 0x1fffffffLL)
+    return fail(TTT_E_UNSUPPORTED, "%s: T > 2^30, or B*H*T/64 or B*H*d exceeds the grid limit", fn);
   return TTT_OK;
 }
 

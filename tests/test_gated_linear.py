@@ -96,7 +96,8 @@ INVALID, UNSUPPORTED = -1, -2
     (dict(H=-1), INVALID), (dict(d=0), INVALID), (dict(eta=float("nan")), INVALID), (dict(eta=float("inf")), INVALID),
     (dict(io=2), INVALID), (dict(k=FAKE + 8), INVALID), (dict(w0=FAKE + 4), INVALID), (dict(gate=FAKE + 2), INVALID),
     (dict(eta_tok=FAKE + 1), INVALID), (dict(d=48), UNSUPPORTED), (dict(d=128), UNSUPPORTED),
-    (dict(B=1 << 20, H=1 << 20), INVALID)])
+    (dict(B=1 << 20, H=1 << 20), INVALID), (dict(B=1 << 18, H=1 << 5, d=64), UNSUPPORTED),
+    (dict(B=1 << 20, H=1 << 5), UNSUPPORTED)])
 def test_refusals(lib, fn, bad, want):
     assert _call(lib, fn, **bad) == want
     assert fn in ttt.last_error()
@@ -204,6 +205,30 @@ def test_ragged_batch(io, d):
         assert_within(n, t, ref[n], tol[n])
     for n in ("z", "dq", "dk", "dv", "dlog_gate", "deta_tok"):
         assert not got[n][0].any() and not got[n][1, :, 1:].any(), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [16, 64])
+def test_tokens_past_the_lengths_are_zero_whatever_the_states_hold(io, d):
+    x = gated_inputs(4, 2, 600, d, io, "soft", rates=True, lengths=[0, 1, 70, 333], seed=26)
+    x["w0"][:] = float("nan")
+    x["dw_out"][:] = float("inf")
+    g = _to_gpu(x)
+    got = {"z": _forward(g)[0], **_backward(g)}
+    for b, n in enumerate([0, 1, 70, 333]):
+        for name in ("z", "dq", "dk", "dv", "dlog_gate", "deta_tok"):
+            assert not got[name][b, :, n:].any(), (name, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [40, 700])
+def test_no_gradient_of_a_gate_whose_decay_is_zero(io, T):
+    x = gated_inputs(2, 3, T, 32, io, "soft", seed=27)
+    x["log_gate"][..., ::7] = -150.0  # 0 in float32, far from the lowest value
+    dg = _backward(_to_gpu(x))["dlog_gate"]
+    assert not dg[..., ::7].any() and dg[..., 1::7].all()
 
 
 @pytest.mark.gpu
