@@ -12,7 +12,8 @@
 //
 // Both are bound by HBM: each tensor passes once (8 x 12 x 2048 rows of 64 bf16 with gate and
 // residual: forward 19 us, 5.3 TB/s; backward 28 us, 4.4 TB/s, where the vector units are half as
-// busy).  A row lives in the registers of LPR lanes (part of a wave, a wave, or a workgroup), NV
+// busy).  Without gate and scale the backward pass is a kernel of its own (kPlain), which needs 40 % fewer
+// registers: 8191 rows of 768 bf16 take 17.3 us and not 22, 8192 of 2048 29.6 and not 44.  A row lives in the registers of LPR lanes (part of a wave, a wave, or a workgroup), NV
 // vectors of W elements a lane, so its statistics need no second read; everything between load and
 // store is float32.
 //
@@ -157,7 +158,7 @@ __device__ __forceinline__ float normalise(float* x, const bool* live, const Pla
 }
 
 template <int LPR> struct Block {
-  static constexpr int kThreads = LPR > 256 ? LPR : 256;
+  static constexpr int kThreads = LPR > 64 ? LPR : 256;
   static constexpr int kRows = kThreads / LPR;  // rows a workgroup holds at once
 };
 
@@ -233,8 +234,12 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_fwd_kernel(NormArgs
 
 // Workgroup (part, head) takes a share of the head's B T rows, and leaves its sums of the
 // parameters' gradients in part[head][part][wanted sums][d].
-template <typename IO, int W, int LPR, int NV, bool A>
+template <typename IO, int W, int LPR, int NV, bool A, bool kPlain>
 __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs a, float* part, int share) {
+  if constexpr (kPlain) {
+    a.gate = a.dgate = nullptr;
+    a.scale = a.dscale = nullptr;
+  }
   extern __shared__ __attribute__((aligned(16))) float sums[];  // [2][wanted sums][d] (rows of a wave or less)
   __shared__ float red[2][16];
   int turn = 0;
@@ -273,9 +278,10 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
       if (gp) next.gt[v].load(gp + next.base + col);
     }
   };
-  if (from < to) fetch(from);
+  constexpr bool kNext = LPR < 1024;  // 1024 threads leave a lane 128 registers: no room for a second row
+  if (kNext && from < to) fetch(from);
   // the head's parameters, kept in registers while they are few
-  constexpr bool kKeep = N <= 24;
+  constexpr bool kKeep = N <= 24 && kNext;
   float wt_[kKeep ? N : W], bs_[kKeep ? N : W], sc_[kKeep ? N : W];
   auto parameters = [&](int col, float* wt, float* bs, float* sc) {
 #pragma unroll
@@ -292,17 +298,19 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
     for (int v = 0; v < NV; ++v) parameters(at[v].col, wt_ + v * W, bs_ + v * W, sc_ + v * W);
   }
   for (int first = from; first < to; first += RB) {
+    if (!kNext) fetch(first);
     const size_t base = next.base;
-    float x[N], dy[N], gt[N];
+    float x[N], dy[N];
+    Vec<IO, W, A> gv[NV];
     bool have[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       have[v] = next.live && at[v].have;
       next.x[v].widen(x + v * W, have[v], at[v].dup);
       next.dy[v].widen(dy + v * W, have[v], at[v].dup);
-      if (gp) next.gt[v].widen(gt + v * W, have[v], at[v].dup);
+      if (gp) gv[v] = next.gt[v];
     }
-    if (first + RB < to) fetch(first + RB);
+    if (kNext && first + RB < to) fetch(first + RB);
     const float r = normalise<W, LPR, NV, A>(x, have, at, a.kind, a.d, a.eps, red, &turn);
     float m1 = 0.0f, m2 = 0.0f;
 #pragma unroll
@@ -312,14 +320,15 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
       float* wt = wt_ + (kKeep ? v * W : 0);
       float* bs = bs_ + (kKeep ? v * W : 0);
       float* sc = sc_ + (kKeep ? v * W : 0);
-      float dg[W];
+      float dg[W], gt[W];
+      if (gp) gv[v].widen(gt, true, at[v].dup);
       if constexpr (!kKeep) parameters(col, wt, bs, sc);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const int j = v * W + i;
         const float n = x[j] * wt[i] + bs[i];
         float act = 1.0f, dact = 0.0f;
-        if (gp) act_grad(a.act, gt[j], &act, &dact);
+        if (gp) act_grad(a.act, gt[i], &act, &dact);
         ss[j] += dy[j] * act * n;
         const float t0 = dy[j] * sc[i], t = t0 * act;
         dg[i] = t0 * n * dact;
@@ -434,12 +443,12 @@ bool vectors(const NormArgs& a, int es) {
          aligned16({a.x, a.weight, a.bias, a.gate, a.scale, a.res, a.y, a.dy, a.dx, a.dgate});
 }
 
-// f(W, LPR, NV) for the smallest layout that holds a row of d elements
-template <int W, typename F>
-hipError_t layout(int d, F f) {
-  const int n = (d + W - 1) / W;
+// f(W, LPR, NV) for the first layout that holds a row of d elements
 #define TTT_TRY(lpr, nv) \
   if (n <= lpr * nv) return f(std::integral_constant<int, W>(), std::integral_constant<int, lpr>(), std::integral_constant<int, nv>())
+template <int W, typename F>
+hipError_t fwd_layout(int d, F f) {
+  const int n = (d + W - 1) / W;
   TTT_TRY(2, 1);
   TTT_TRY(4, 1);
   TTT_TRY(8, 1);
@@ -458,16 +467,47 @@ hipError_t layout(int d, F f) {
     if constexpr (W == 8) TTT_TRY(1024, 2);
     if constexpr (W == 4) TTT_TRY(1024, 4);
   }
-#undef TTT_TRY
   return hipErrorInvalidValue;
 }
+// The backward pass holds three more rows (the parameters' sums) and the next one: no more than 16
+// elements a lane, so that two waves share a SIMD's registers.  With a gate, us: 8191 rows of
+// 768 bf16 as 64 x 2 vectors 23.3, as 32 x 3 32.4; 8192 of 2048 as 256 x 1 47.7, as 64 x 4 70.8; 8192 of
+// 4096 as 256 x 2 77.6, as 512 x 1 91.3.  Rows of 8193 to 12288 bf16 are 512 x 3: 56.7 us for 2048
+// of 12000, as 1024 x 2 71.8 (with a gate 276 and 282: the registers spill in both).
+template <int W, typename F>
+hipError_t bwd_layout(int d, F f) {
+  const int n = (d + W - 1) / W;
+  TTT_TRY(2, 1);
+  TTT_TRY(4, 1);
+  TTT_TRY(8, 1);
+  if constexpr (W > 1) {
+    TTT_TRY(16, 1);
+    TTT_TRY(32, 1);
+    TTT_TRY(64, 1);
+    TTT_TRY(64, 2);
+    TTT_TRY(256, 1);
+    TTT_TRY(256, 2);
+    TTT_TRY(512, 2);
+    if constexpr (W == 8) TTT_TRY(512, 3);
+    if constexpr (W == 8) TTT_TRY(1024, 2);
+    if constexpr (W == 4) TTT_TRY(512, 4);
+    if constexpr (W == 4) TTT_TRY(1024, 4);
+  }
+  return hipErrorInvalidValue;
+}
+#undef TTT_TRY
 // whole rows of aligned vectors, else vectors at any element, else (rows shorter than one) elements
-template <typename IO, typename F>
+template <typename IO, bool kBwd, typename F>
 hipError_t choose(const NormArgs& a, F f) {
   constexpr int W = 16 / static_cast<int>(sizeof(IO));
-  if (vectors(a, sizeof(IO))) return layout<W>(a.d, [&](auto w, auto lpr, auto nv) { return f(w, lpr, nv, std::true_type()); });
-  if (a.d >= W) return layout<W>(a.d, [&](auto w, auto lpr, auto nv) { return f(w, lpr, nv, std::false_type()); });
-  return layout<1>(a.d, [&](auto w, auto lpr, auto nv) { return f(w, lpr, nv, std::true_type()); });
+  const auto layout = [&](auto w, auto al) {
+    const auto g = [&](auto w, auto lpr, auto nv) { return f(w, lpr, nv, al); };
+    if constexpr (kBwd) return bwd_layout<w.value>(a.d, g);
+    else return fwd_layout<w.value>(a.d, g);
+  };
+  if (vectors(a, sizeof(IO))) return layout(std::integral_constant<int, W>(), std::true_type());
+  if (a.d >= W) return layout(std::integral_constant<int, W>(), std::false_type());
+  return layout(std::integral_constant<int, 1>(), std::true_type());
 }
 
 template <typename IO, int W, int LPR, int NV, bool A>
@@ -485,13 +525,16 @@ hipError_t run_fwd(const NormArgs& a, hipStream_t s) {
 
 // The backward pass's workgroups: at most 768 (three of 256 threads a CU, so that all start at
 // once and end together), each with 16 rows of a head at least so that its sums stay small next to
-// its rows.  On 8 x 12 x 2048 rows of 64 bf16: 512 workgroups 33.5 us, 768 28.5, 1024 34.7, 1536 31.2;
-// on 8191 rows of 768: 256 workgroups 20.2 us, 512 16.3, 1024 18.7.
+// its rows, or 4 while there are less than 256, one a CU.  On 8 x 12 x 2048 rows of 64 bf16 with a
+// gate: 512 workgroups 33.7 us, 768 28.8, 1024 34.7; on 8192 of 2048 without: 512 of them (16 rows)
+// 27.3, 768 33.6; on 2048 of 8192: 128 (16 rows) 38.8, 256 27.8; on 1024 of 16384 float32: 64 (16
+// rows) 101, 128 66, 256 54.
 long long most_parts(int B, int H, int T) {
   const long long rows = static_cast<long long>(B) * T;
-  long long parts = 768 / H;
-  if (parts > (rows + 15) / 16) parts = (rows + 15) / 16;
-  return parts < 1 ? 1 : parts;
+  const long long of16 = (rows + 15) / 16, of4 = (rows + 3) / 4, one_a_cu = 256 / H;
+  const long long parts = of16 > one_a_cu ? of16 : of4 < one_a_cu ? of4 : one_a_cu;
+  const long long most = 768 / H < parts ? 768 / H : parts;
+  return most < 1 ? 1 : most;
 }
 // rows of a part: whole passes of `at_once` rows
 int rows_of_part(int B, int H, int T, int at_once) {
@@ -504,13 +547,13 @@ int bwd_parts(int B, int H, int T, int share) {
   return static_cast<int>(parts < 1 ? 1 : parts);
 }
 
-template <typename IO, int W, int LPR, int NV, bool A>
+template <typename IO, int W, int LPR, int NV, bool A, bool kPlain>
 hipError_t run_bwd(const NormArgs& a, void* ws, hipStream_t s) {
   const int share = rows_of_part(a.B, a.H, a.T, Block<LPR>::kRows), parts = bwd_parts(a.B, a.H, a.T, share);
   const bool sums = a.dweight || a.dbias || a.dscale;
   const int lds = sums && LPR <= 64 ? 2 * 3 * a.d * static_cast<int>(sizeof(float)) : 0;  // 48 KB at most
   float* part = sums ? static_cast<float*>(ws) : nullptr;
-  norm_bwd_kernel<IO, W, LPR, NV, A><<<dim3(parts, a.H), dim3(Block<LPR>::kThreads), lds, s>>>(a, part, share);
+  norm_bwd_kernel<IO, W, LPR, NV, A, kPlain><<<dim3(parts, a.H), dim3(Block<LPR>::kThreads), lds, s>>>(a, part, share);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !sums) return e;
   norm_sum_kernel<<<dim3((a.d + 31) / 32, a.H, 3), dim3(1024), 0, s>>>(a, part, parts);
@@ -519,12 +562,15 @@ hipError_t run_bwd(const NormArgs& a, void* ws, hipStream_t s) {
 
 template <typename IO>
 hipError_t bwd_io(const NormArgs& a, void* ws, hipStream_t s) {
-  return choose<IO>(a, [&](auto w, auto lpr, auto nv, auto al) { return run_bwd<IO, w.value, lpr.value, nv.value, al.value>(a, ws, s); });
+  return choose<IO, true>(a, [&](auto w, auto lpr, auto nv, auto al) {
+    if (a.gate || a.scale) return run_bwd<IO, w.value, lpr.value, nv.value, al.value, false>(a, ws, s);
+    return run_bwd<IO, w.value, lpr.value, nv.value, al.value, true>(a, ws, s);
+  });
 }
 
 template <typename IO>
 hipError_t fwd_io(const NormArgs& a, hipStream_t s) {
-  return choose<IO>(a, [&](auto w, auto lpr, auto nv, auto al) { return run_fwd<IO, w.value, lpr.value, nv.value, al.value>(a, s); });
+  return choose<IO, false>(a, [&](auto w, auto lpr, auto nv, auto al) { return run_fwd<IO, w.value, lpr.value, nv.value, al.value>(a, s); });
 }
 
 }  // namespace

@@ -109,6 +109,15 @@ def test_wide_rows(io, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("parts", ["wb", "wbg"])
+@pytest.mark.parametrize("d", [5, 65, 768, 1032, 2052, 4100, 8200, 12288, 16384])
+def test_several_rows_of_every_width(io, parts, d):
+    """More rows than a workgroup holds at once, with and without a gate."""
+    _check(*_inputs(2, 2, 33, d, io, parts, seed=d), "layer")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("parts", ["", "w", "wb", "g", "ws", "r", "wgsr", "wbgs"])
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "sigmoid"])
 def test_parts(parts, act):
