@@ -11,7 +11,7 @@
 // the tokens.
 //
 // Both are bound by HBM: each tensor passes once (8 x 12 x 2048 rows of 64 bf16 with gate and
-// residual: forward 19 us, 5.3 TB/s; backward 28 us, 4.4 TB/s, where the vector units are half as
+// residual: forward 19 us, 5.3 TB/s; backward 28 us, 4.4 TB/s, where the vector units are 80 %
 // busy).  Without gate and scale the backward pass is a kernel of its own (kPlain), which needs 40 % fewer
 // registers: 8191 rows of 768 bf16 take 17.3 us and not 22, 8192 of 2048 29.6 and not 44.  A row lives in the registers of LPR lanes (part of a wave, a wave, or a workgroup), NV
 // vectors of W elements a lane, so its statistics need no second read; everything between load and
