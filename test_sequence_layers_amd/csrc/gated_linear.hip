@@ -77,10 +77,18 @@ struct Math<float> {
     }
     return c;
   }
-  template <int N> static __device__ __forceinline__ Parts<N> split(const gl_f4& a, const gl_f4& b) { return Parts<N>{Op{a, b}}; }
-    // the parts as rows (A), as columns (B)
-  template <int N, bool Half> static __device__ __forceinline__ gl_f4 mma_rows(const Parts<N>& a, const Op& b, gl_f4 c) { return mma<Half>(a.x, b, c); }
-  template <int N, bool Half> static __device__ __forceinline__ gl_f4 mma_cols(const Op& a, const Parts<N>& b, gl_f4 c) { return mma<Half>(a, b.x, c); }
+  template <int N> static __device__ __forceinline__ Parts<N> split(const gl_f4& a, const gl_f4& b) {
+    return Parts<N>{Op{a, b}};
+  }
+  // the parts as rows (A), as columns (B)
+  template <int N, bool Half>
+  static __device__ __forceinline__ gl_f4 mma_rows(const Parts<N>& a, const Op& b, gl_f4 c) {
+    return mma<Half>(a.x, b, c);
+  }
+  template <int N, bool Half>
+  static __device__ __forceinline__ gl_f4 mma_cols(const Op& a, const Parts<N>& b, gl_f4 c) {
+    return mma<Half>(a, b.x, c);
+  }
   static __device__ __forceinline__ void widen(const Op& x, gl_f4* a, gl_f4* b) {
     *a = x.a;
     *b = x.b;
@@ -102,10 +110,13 @@ struct Math<float> {
   // feature of row 4 g of tile b of a state
   template <int D> static __device__ __forceinline__ int state_row(int b, int g) { return 16 * b + 4 * g; }
   // the same features of a token tile as rows of an operand, k down the tokens
-  template <int D> static __device__ __forceinline__ Op down_state(const float* m, int ld, int p, int b, int g, int r) {
+  template <int D>
+  static __device__ __forceinline__ Op down_state(const float* m, int ld, int p, int b, int g, int r) {
     return down<D>(m, ld, p, b, g, r);
   }
-  template <int D> static __device__ __forceinline__ gl_f4 row4(const float* row, int cb, int g) { return at4(row, 16 * cb + 4 * g); }
+  template <int D> static __device__ __forceinline__ gl_f4 row4(const float* row, int cb, int g) {
+    return at4(row, 16 * cb + 4 * g);
+  }
   typedef gl_f4 Four;  // four features of a token, from element `elem` of the source
   static __device__ __forceinline__ Four load4(__amdgpu_buffer_rsrc_t src, int elem) {
     return __builtin_bit_cast(gl_f4, __builtin_amdgcn_raw_buffer_load_b128(src, elem * 4, 0, 0));
@@ -157,13 +168,15 @@ struct Math<bf16> {
   template <int D> static __device__ __forceinline__ int state_row(int b, int g) {
     return D == 16 ? 4 * g : 32 * (b >> 1) + 8 * g + 4 * (b & 1);
   }
-  template <int D> static __device__ __forceinline__ Op down_state(const bf16* m, int ld, int p, int b, int g, int r) {
+  template <int D>
+  static __device__ __forceinline__ Op down_state(const bf16* m, int ld, int p, int b, int g, int r) {
     return down_at(m, ld, p, state_row<D>(b, r & 3), g, r);
   }
   template <bool Half> static __device__ __forceinline__ gl_f4 mma(const Op& a, const Op& b, gl_f4 c) {
     if constexpr (Half) {
       const gl_b4 x = __builtin_shufflevector(a, a, 0, 1, 2, 3), y = __builtin_shufflevector(b, b, 0, 1, 2, 3);
-      return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(gl_s4, x), __builtin_bit_cast(gl_s4, y), c, 0, 0, 0);
+      return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(gl_s4, x), __builtin_bit_cast(gl_s4, y),
+                                                       c, 0, 0, 0);
     }
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -187,12 +200,14 @@ struct Math<bf16> {
     return y;
   }
   // the parts as rows (A), as columns (B), small ones first
-  template <int N, bool Half> static __device__ __forceinline__ gl_f4 mma_rows(const Parts<N>& a, const Op& b, gl_f4 c) {
+  template <int N, bool Half>
+  static __device__ __forceinline__ gl_f4 mma_rows(const Parts<N>& a, const Op& b, gl_f4 c) {
 #pragma unroll
     for (int n = N - 1; n >= 0; --n) c = mma<Half>(a.x[n], b, c);
     return c;
   }
-  template <int N, bool Half> static __device__ __forceinline__ gl_f4 mma_cols(const Op& a, const Parts<N>& b, gl_f4 c) {
+  template <int N, bool Half>
+  static __device__ __forceinline__ gl_f4 mma_cols(const Op& a, const Parts<N>& b, gl_f4 c) {
 #pragma unroll
     for (int n = N - 1; n >= 0; --n) c = mma<Half>(a, b.x[n], c);
     return c;
@@ -213,10 +228,12 @@ struct Math<bf16> {
         gl_u4{a, b, gl_pack(x[0] - gl_lo(a), x[1] - gl_hi(a)), gl_pack(x[2] - gl_lo(b), x[3] - gl_hi(b))};
   }
   static __device__ __forceinline__ Block block(const Op& x, int half) {
-    return half ? __builtin_shufflevector(x, x, 4, 5, 6, 7, 4, 5, 6, 7) : __builtin_shufflevector(x, x, 0, 1, 2, 3, 0, 1, 2, 3);
+    return half ? __builtin_shufflevector(x, x, 4, 5, 6, 7, 4, 5, 6, 7)
+                : __builtin_shufflevector(x, x, 0, 1, 2, 3, 0, 1, 2, 3);
   }
   static __device__ __forceinline__ gl_f4 mma_factor(const Block& a, const bf16* row, int cb, int g, gl_f4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, *reinterpret_cast<const gl_b8*>(row + 32 * cb + 8 * g), c, 0, 0, 0);
+    const gl_b8 b = *reinterpret_cast<const gl_b8*>(row + 32 * cb + 8 * g);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
   // columns 16 cb + 4 g .. + 3 of a row, from a 16-byte read that two g share
   template <int D> static __device__ __forceinline__ gl_f4 row4(const bf16* row, int cb, int g) {
@@ -227,7 +244,9 @@ struct Math<bf16> {
   static __device__ __forceinline__ Four load4(__amdgpu_buffer_rsrc_t src, int elem) {
     return __builtin_amdgcn_raw_buffer_load_b64(src, elem * 2, 0, 0);
   }
-  static __device__ __forceinline__ gl_f4 widen4(const Four& w) { return gl_f4{gl_lo(w[0]), gl_hi(w[0]), gl_lo(w[1]), gl_hi(w[1])}; }
+  static __device__ __forceinline__ gl_f4 widen4(const Four& w) {
+    return gl_f4{gl_lo(w[0]), gl_hi(w[0]), gl_lo(w[1]), gl_hi(w[1])};
+  }
   static __device__ __forceinline__ void store4(const gl_f4& x, __amdgpu_buffer_rsrc_t dst, int elem) {
     const gl_u2 y = {gl_pack(x[0], x[1]), gl_pack(x[2], x[3])};
     __builtin_amdgcn_raw_buffer_store_b64(y, dst, elem * 2, 0, 0);
@@ -271,6 +290,12 @@ __device__ __forceinline__ typename Math<IO>::Elem* factor_row(typename Math<IO>
   return m + 16 * (B * (t * (t + 1) / 2) + P * t) + r * (B * (t + 1) + P);
 }
 
+// tokens c0 .. of a tensor of D features, `rows` of them (none if negative)
+template <int D, typename IO>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t token_span(const IO* base, long long c0, int rows) {
+  return gl_span(base + c0 * D, max(0, min(kC, rows)) * D * static_cast<int>(sizeof(IO)));
+}
+
 // Loads.  A tile's registers are filled by buffer loads whose range ends at the last valid token
 // (0 bytes for a chunk outside the segment), so every wave issues the same ones on every path.
 // Loads and stores complete in order: a wait for a load issued before some stores need not wait for
@@ -283,7 +308,7 @@ struct Tile {
   gl_u4 x[kVec];
   // tokens c0 .. of base, `rows` of them valid (may be negative)
   __device__ __forceinline__ void load(const IO* base, long long c0, int rows, int tid) {
-    const __amdgpu_buffer_rsrc_t src = gl_span(base + c0 * D, max(0, min(kC, rows)) * D * static_cast<int>(sizeof(IO)));
+    const __amdgpu_buffer_rsrc_t src = token_span<D>(base, c0, rows);
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
       x[i] = __builtin_amdgcn_raw_buffer_load_b128(src, (tid + i * kThreads) * 16, 0, 0);
@@ -338,7 +363,6 @@ __device__ __forceinline__ const float* initial_state(const GatedArgs& a, int ch
   return a.w0 + (chain / a.H) * a.w0_batch_stride + static_cast<size_t>(chain % a.H) * dd;
 }
 
-
 // A state in registers: row 4 g + e of tile b and column r of wave wv are the elements (f + e,
 // 16 wv + r), f = state_row(b, g), of W, or of W^T (kTransposed).
 template <typename IO, int D, bool kTransposed>
@@ -392,11 +416,13 @@ template <typename IO, int D, int N>
 __device__ __forceinline__ void split_state(typename Math<IO>::template Parts<N>* y, const gl_f4* x) {
 #pragma unroll
   for (int p = 0; p < Shape<IO, D>::kNP; ++p)
-    y[p] = Math<IO>::template split<N>(x[2 * p], Shape<IO, D>::kHalf ? gl_f4{0.0f, 0.0f, 0.0f, 0.0f} : x[Shape<IO, D>::kHalf ? 0 : 2 * p + 1]);
+    y[p] = Math<IO>::template split<N>(
+        x[2 * p], Shape<IO, D>::kHalf ? gl_f4{0.0f, 0.0f, 0.0f, 0.0f} : x[Shape<IO, D>::kHalf ? 0 : 2 * p + 1]);
 }
 // rows of the state times a token's row: C[16 rows][16 tokens]
 template <typename IO, int D, int N>
-__device__ __forceinline__ gl_f4 state_times(const typename Math<IO>::template Parts<N>* w, const typename Math<IO>::Elem* row, int g) {
+__device__ __forceinline__ gl_f4 state_times(const typename Math<IO>::template Parts<N>* w,
+                                             const typename Math<IO>::Elem* row, int g) {
   typedef Shape<IO, D> S;
   gl_f4 c = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -406,12 +432,14 @@ __device__ __forceinline__ gl_f4 state_times(const typename Math<IO>::template P
 }
 // C[16 tokens of a][16 tokens of b]: products of rows
 template <typename IO, int D>
-__device__ __forceinline__ gl_f4 row_products(const typename Math<IO>::Elem* a, const typename Math<IO>::Elem* b, int g) {
+__device__ __forceinline__ gl_f4 row_products(const typename Math<IO>::Elem* a, const typename Math<IO>::Elem* b,
+                                              int g) {
+  typedef Math<IO> M;
   typedef Shape<IO, D> S;
   gl_f4 c = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int p = 0; p < S::kNP; ++p)
-    c = Math<IO>::template mma<S::kHalf>(Math<IO>::template along<S::kHalf>(a, p, g), Math<IO>::template along<S::kHalf>(b, p, g), c);
+    c = M::template mma<S::kHalf>(M::template along<S::kHalf>(a, p, g), M::template along<S::kHalf>(b, p, g), c);
   return c;
 }
 
@@ -475,7 +503,8 @@ __global__ __launch_bounds__(4 * D) void gl_sums_kernel(GatedArgs a) {
     gl_barrier();
     fetch(i + 1);
     const GlDecays& dec = L.dec[i & 1];
-    if (decayer && i + 1 < n) gr.decays(s, a.eta, static_cast<long long>(chunk(i + 1)) * kC, &L.dec[(i + 1) & 1], lane);
+    if (decayer && i + 1 < n)
+      gr.decays(s, a.eta, static_cast<long long>(chunk(i + 1)) * kC, &L.dec[(i + 1) & 1], lane);
     typename M::Op b[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p) b[p] = M::template down<D>(L.b, S::kLd, p, wv, g, r);
@@ -502,7 +531,9 @@ __global__ __launch_bounds__(256) void gl_scan_kernel(GatedArgs a) {
   const size_t seg0 = static_cast<size_t>(chain) * a.nseg;
   float* x = (side == 0 ? a.seg_w : a.seg_g) + seg0 * D * D + at;
   const float* decay = a.seg_decay + static_cast<size_t>(side) * a.B * a.H * a.nseg + seg0;
-  const float* start = side == 0 ? initial_state(a, chain, D * D) : a.dw_out ? a.dw_out + static_cast<size_t>(chain) * D * D : nullptr;
+  const float* start = side == 0  ? initial_state(a, chain, D * D)
+                       : a.dw_out ? a.dw_out + static_cast<size_t>(chain) * D * D
+                                  : nullptr;
   vec state = 0.0f;
   if (start) state = *reinterpret_cast<const vec*>(start + at);
   for (int i0 = 0; i0 < a.nseg; i0 += kAhead) {
@@ -600,7 +631,8 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
     const GateRate gr = y.gr;
     gl_barrier();
     fetch(c + 1);
-    if (decayer && c + 1 < end) gr.decays(s, a.eta, static_cast<long long>(c + 1) * kC, &L.dec[(c + 1 - first) & 1], lane);
+    if (decayer && c + 1 < end)
+      gr.decays(s, a.eta, static_cast<long long>(c + 1) * kC, &L.dec[(c + 1 - first) & 1], lane);
 
     // P[u][s] = exp(b_u - b_s) e_s (q_u . k_s) for s <= u
     wave_blocks<NW>(wv, [&](auto n, int first_block) {
@@ -635,19 +667,21 @@ __global__ __launch_bounds__(4 * D) void gl_fwd_kernel(GatedArgs a) {
     for (int p = 0; p < 2; ++p) vf[p] = M::template down<D>(L.v, LD, p, wv, g, r);
     typename M::template Parts<2> wp[S::kNP];
     split_state<IO, D, 2>(wp, w);
-    const __amdgpu_buffer_rsrc_t dst = gl_span(z + static_cast<size_t>(c0) * D, min(kC, T - c0) * D * static_cast<int>(sizeof(IO)));
+    const __amdgpu_buffer_rsrc_t dst = token_span<D>(z, c0, T - c0);
 #pragma unroll
     for (int ut = 0; ut < 4; ++ut) {  // Z^T: rows j, columns u
       const int u = 16 * ut + r;
       const gl_f4 zi = state_times<IO, D, 2>(wp, L.q + u * LD, g);
       gl_f4 zp = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int st = 0; st <= ut; ++st) zp = M::mma_factor(M::block(vf[st / 2], st % 2), factor_row<IO>(L.p, ut, r), st, g, zp);
+      for (int st = 0; st <= ut; ++st)
+        zp = M::mma_factor(M::block(vf[st / 2], st % 2), factor_row<IO>(L.p, ut, r), st, g, zp);
       M::store4(zp + keep4(dec.from[u], zi), dst, u * D + 16 * wv + 4 * g);
     }
     update_state<IO, D, 3>(w, dec.whole[0], L.k, vf, dec.to_e, g, r);
   }
-  if (a.w_out && seg == a.nseg - 1) store_state_transposed<IO, D>(w, a.w_out + static_cast<size_t>(chain) * D * D, wv, g, r);
+  if (a.w_out && seg == a.nseg - 1)
+    store_state_transposed<IO, D>(w, a.w_out + static_cast<size_t>(chain) * D * D, wv, g, r);
 }
 
 // ---------------------------------------------------------------- backward
@@ -748,7 +782,7 @@ __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
     const GateRate gr = y.gr;
     // the wave's features of Q, for in_u
     typename M::Four qu[4];
-    const __amdgpu_buffer_rsrc_t qsrc = gl_span(q + static_cast<size_t>(c0) * D, in_o ? max(0, min(kC, s.len - c0)) * D * static_cast<int>(sizeof(IO)) : 0);
+    const __amdgpu_buffer_rsrc_t qsrc = token_span<D>(q, c0, in_o ? s.len - c0 : 0);
 #pragma unroll
     for (int ut = 0; ut < 4; ++ut) qu[ut] = M::load4(qsrc, (16 * ut + r) * D + 16 * wv + 4 * g);
     gl_barrier();
@@ -785,14 +819,15 @@ __global__ __launch_bounds__(4 * D) void gl_dq_kernel(GatedArgs a) {
     for (int p = 0; p < 2; ++p) kf[p] = M::template down<D>(L.k, LD, p, wv, g, r);
     typename M::template Parts<3> wp[S::kNP];
     split_state<IO, D, 3>(wp, w);
-    const __amdgpu_buffer_rsrc_t dst = gl_span(dq + static_cast<size_t>(c0) * D, min(kC, T - c0) * D * static_cast<int>(sizeof(IO)));
+    const __amdgpu_buffer_rsrc_t dst = token_span<D>(dq, c0, T - c0);
 #pragma unroll
     for (int ut = 0; ut < 4; ++ut) {
       const int u = 16 * ut + r;
       const gl_f4 xi = keep4(dec.from[u], state_times<IO, D, 3>(wp, L.z + u * LD, g));
       gl_f4 xp = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int st = 0; st <= ut; ++st) xp = M::mma_factor(M::block(kf[st / 2], st % 2), factor_row<IO>(L.r, ut, r), st, g, xp);
+      for (int st = 0; st <= ut; ++st)
+        xp = M::mma_factor(M::block(kf[st / 2], st % 2), factor_row<IO>(L.r, ut, r), st, g, xp);
       const float in = over_g(dot4(M::widen4(qu[ut]), xi));
       if (g == 0) L.part[wv][u] = in;
       M::store4(xi + xp, dst, u * D + 16 * wv + 4 * g);
@@ -909,7 +944,8 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
     const int c0 = c * kC, bytes = teller && c < end ? min(kC, T - c0) * 4 : 0;
     float dg = 0.0f;
     if (dg_o && teller && c < end) {
-      const double suf = gl_prefix(static_cast<double>(t.row) - t.col + t.in), pre = gl_prefix(static_cast<double>(t.out));
+      const double suf = gl_prefix(static_cast<double>(t.row) - t.col + t.in);
+      const double pre = gl_prefix(static_cast<double>(t.out));
       const double in = gl_prefix(static_cast<double>(t.in));
       const double past = later - __shfl(pre, 63, 64);
       const double from_here = __shfl(suf, 63, 64) - suf + (static_cast<double>(t.row) - t.col + t.in);
@@ -1013,7 +1049,7 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
       }
     });
     gl_barrier();
-    const __amdgpu_buffer_rsrc_t dst = gl_span(out + static_cast<size_t>(c0) * D, min(kC, T - c0) * D * static_cast<int>(sizeof(IO)));
+    const __amdgpu_buffer_rsrc_t dst = token_span<D>(out, c0, T - c0);
     // rows: the tile that the state multiplies; near, far: the tiles of the state's update;
     // f: the chunk's factor; N: the state's parts
     auto rest = [&](auto n, const typename S::Elem* rows, const typename S::Elem* near, const typename S::Elem* far,
@@ -1030,7 +1066,8 @@ __global__ __launch_bounds__(8 * D, 4) void gl_dkv_kernel(GatedArgs a) {
         const gl_f4 xi = keep4(dec.to[ss], state_times<IO, D, N>(xp, rows + ss * LD, g));
         gl_f4 xc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int ut = st; ut < 4; ++ut) xc = M::mma_factor(M::block(b[ut / 2], ut % 2), factor_row<IO>(f, 3 - st, r), ut - st, g, xc);
+        for (int ut = st; ut < 4; ++ut)
+          xc = M::mma_factor(M::block(b[ut / 2], ut % 2), factor_row<IO>(f, 3 - st, r), ut - st, g, xc);
         if constexpr (N == 3) {  // dv
           const float o = over_g(dot4(M::template row4<D>(L.v + ss * LD, wv, g), xi));
           if (g == 0) L.part[wv][ss] = o;
@@ -1081,8 +1118,8 @@ void plan(GatedArgs* a, bool bwd) {
 
 template <typename F>
 hipError_t allow_lds(F fn, int bytes) {
-  return bytes <= 64 * 1024 ? hipSuccess
-                            : hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (bytes <= 64 * 1024) return hipSuccess;
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 template <typename IO, int D>
@@ -1098,7 +1135,8 @@ hipError_t segment_states(const GatedArgs& a, int sides, hipStream_t s) {
   if (e != hipSuccess) return e;
   // four elements a thread once that still fills the chip (256 CUs of 2048 threads)
   const long long quads = static_cast<long long>(chains) * (D * D / 4) * sides;
-  if (quads >= 256 * 512) gl_scan_kernel<D, 4><<<dim3(static_cast<unsigned>((quads / sides + 255) / 256), sides), dim3(256), 0, s>>>(a);
+  const unsigned groups = static_cast<unsigned>((quads / sides + 255) / 256);
+  if (quads >= 256 * 512) gl_scan_kernel<D, 4><<<dim3(groups, sides), dim3(256), 0, s>>>(a);
   else gl_scan_kernel<D, 1><<<dim3(chains * (D * D / 256), sides), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }

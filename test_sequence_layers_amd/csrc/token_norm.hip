@@ -12,10 +12,11 @@
 //
 // Both are bound by HBM: each tensor passes once (8 x 12 x 2048 rows of 64 bf16 with gate and
 // residual: forward 19 us, 5.3 TB/s; backward 28 us, 4.4 TB/s, where the vector units are 80 %
-// busy).  Without gate and scale the backward pass is a kernel of its own (kPlain), which needs 40 % fewer
-// registers: 8191 rows of 768 bf16 take 17.3 us and not 22, 8192 of 2048 29.6 and not 44.  A row lives in the registers of LPR lanes (part of a wave, a wave, or a workgroup), NV
-// vectors of W elements a lane, so its statistics need no second read; everything between load and
-// store is float32.
+// busy).  Without gate and scale the backward pass is a kernel of its own (kPlain), which needs
+// 40 % fewer registers: 8191 rows of 768 bf16 take 17.3 us and not 22, 8192 of 2048 29.6 and not 44.
+// A row lives in the registers of LPR lanes (part of a wave, a wave, or a workgroup), NV vectors of
+// W elements a lane, so its statistics need no second read; everything between load and store is
+// float32.
 //
 // A vector is 16 bytes.  Where rows or tensors are not aligned to that (`A` false) its loads and
 // stores are not either, and the last vector of a row begins early, at d - W: its first `dup`
@@ -84,7 +85,8 @@ struct Places {
   Place<W, LPR, A> p[NV];
   __device__ __forceinline__ Places(int in_row, int d) : Places(in_row, d, std::make_integer_sequence<int, NV>()) {}
   template <int... V>
-  __device__ __forceinline__ Places(int in_row, int d, std::integer_sequence<int, V...>) : p{Place<W, LPR, A>(V, in_row, d)...} {}
+  __device__ __forceinline__ Places(int in_row, int d, std::integer_sequence<int, V...>)
+      : p{Place<W, LPR, A>(V, in_row, d)...} {}
 };
 // float32 parameters of the same W columns (16 bytes at a time when W > 1)
 template <int W, bool A>
@@ -136,8 +138,8 @@ __device__ __forceinline__ float row_sum(float x, float (*red)[16], int* turn) {
 
 // The row in registers: x becomes xh; returns r.
 template <int W, int LPR, int NV, bool A>
-__device__ __forceinline__ float normalise(float* x, const bool* live, const Place<W, LPR, A>* at, int kind, int d, float eps,
-                                           float (*red)[16], int* turn) {
+__device__ __forceinline__ float normalise(float* x, const bool* live, const Place<W, LPR, A>* at, int kind,
+                                           int d, float eps, float (*red)[16], int* turn) {
   constexpr int N = NV * W;
   const float inv = kind == kL2 ? 1.0f : 1.0f / d;
   if (kind == kLayer) {
@@ -268,8 +270,9 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
   } next;
   auto fetch = [&](int first) {
     next.live = first + group < to;
-    const unsigned bt = next.live ? first + group : 0, b = bt / static_cast<unsigned>(a.T);  // a valid row in any case
-    next.base = (static_cast<size_t>(b * static_cast<unsigned>(a.H) + head) * a.T + (bt - b * static_cast<unsigned>(a.T))) * a.d;
+    const unsigned bt = next.live ? first + group : 0;  // a valid row in any case
+    const unsigned b = bt / static_cast<unsigned>(a.T), t = bt - b * static_cast<unsigned>(a.T);
+    next.base = (static_cast<size_t>(b * static_cast<unsigned>(a.H) + head) * a.T + t) * a.d;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int col = at[v].col;
@@ -394,7 +397,8 @@ __global__ __launch_bounds__(Block<LPR>::kThreads) void norm_bwd_kernel(NormArgs
 #pragma unroll
     for (int half = Block<LPR>::kThreads / 128; half > 0; half >>= 1) {
       float* slot = sums + (wave % half) * all_sums;
-      if (mine && wave >= half && wave < 2 * half) columns([&](int i, piece& x) { *reinterpret_cast<piece*>(slot + i) = x; });
+      if (mine && wave >= half && wave < 2 * half)
+        columns([&](int i, piece& x) { *reinterpret_cast<piece*>(slot + i) = x; });
       __syncthreads();
       if (mine && wave < half) columns([&](int i, piece& x) { x += *reinterpret_cast<const piece*>(slot + i); });
       __syncthreads();
@@ -419,7 +423,8 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs a, const float*
   if (col < a.d) {
     const int before[3] = {0, a.dweight ? 1 : 0, (a.dweight ? 1 : 0) + (a.dbias ? 1 : 0)};
     const size_t pitch = static_cast<size_t>(before[2] + (a.dscale ? 1 : 0)) * a.d;
-    const float* p = part + static_cast<size_t>(head) * parts * pitch + static_cast<size_t>(before[which]) * a.d + col;
+    const float* p = part + static_cast<size_t>(head) * parts * pitch;
+    p += static_cast<size_t>(before[which]) * a.d + col;
 #pragma unroll 8
     for (int i = q; i < parts; i += 32) s += p[i * pitch];
   }
@@ -444,8 +449,9 @@ bool vectors(const NormArgs& a, int es) {
 }
 
 // f(W, LPR, NV) for the first layout that holds a row of d elements
+template <int N> using Int = std::integral_constant<int, N>;
 #define TTT_TRY(lpr, nv) \
-  if (n <= lpr * nv) return f(std::integral_constant<int, W>(), std::integral_constant<int, lpr>(), std::integral_constant<int, nv>())
+  if (n <= lpr * nv) return f(Int<W>(), Int<lpr>(), Int<nv>())
 template <int W, typename F>
 hipError_t fwd_layout(int d, F f) {
   const int n = (d + W - 1) / W;
@@ -505,9 +511,9 @@ hipError_t choose(const NormArgs& a, F f) {
     if constexpr (kBwd) return bwd_layout<w.value>(a.d, g);
     else return fwd_layout<w.value>(a.d, g);
   };
-  if (vectors(a, sizeof(IO))) return layout(std::integral_constant<int, W>(), std::true_type());
-  if (a.d >= W) return layout(std::integral_constant<int, W>(), std::false_type());
-  return layout(std::integral_constant<int, 1>(), std::true_type());
+  if (vectors(a, sizeof(IO))) return layout(Int<W>(), std::true_type());
+  if (a.d >= W) return layout(Int<W>(), std::false_type());
+  return layout(Int<1>(), std::true_type());
 }
 
 template <typename IO, int W, int LPR, int NV, bool A>
@@ -518,8 +524,8 @@ hipError_t run_fwd(const NormArgs& a, hipStream_t s) {
   // several passes share a workgroup's start once there are workgroups enough
   // (and a grid holds less than 2^32 threads: at most 2^21 workgroups of 1024)
   const int passes = groups >= 8192 ? static_cast<int>(groups >> 21) + 4 : groups >= 4096 ? 2 : 1;
-  norm_fwd_kernel<IO, W, LPR, NV, A><<<dim3(static_cast<unsigned>((groups + passes - 1) / passes)), dim3(Block<LPR>::kThreads), 0, s>>>(
-      a, static_cast<int>(rows), passes);
+  const dim3 grid(static_cast<unsigned>((groups + passes - 1) / passes)), block(Block<LPR>::kThreads);
+  norm_fwd_kernel<IO, W, LPR, NV, A><<<grid, block, 0, s>>>(a, static_cast<int>(rows), passes);
   return hipGetLastError();
 }
 
@@ -551,9 +557,10 @@ template <typename IO, int W, int LPR, int NV, bool A, bool kPlain>
 hipError_t run_bwd(const NormArgs& a, void* ws, hipStream_t s) {
   const int share = rows_of_part(a.B, a.H, a.T, Block<LPR>::kRows), parts = bwd_parts(a.B, a.H, a.T, share);
   const bool sums = a.dweight || a.dbias || a.dscale;
-  const int lds = sums && LPR <= 64 ? 2 * 3 * a.d * static_cast<int>(sizeof(float)) : 0;  // 48 KB at most
+  const int lds = sums && LPR <= 64 ? 2 * 3 * a.d * static_cast<int>(sizeof(float)) : 0;  // 24 KB at most
   float* part = sums ? static_cast<float*>(ws) : nullptr;
-  norm_bwd_kernel<IO, W, LPR, NV, A, kPlain><<<dim3(parts, a.H), dim3(Block<LPR>::kThreads), lds, s>>>(a, part, share);
+  const dim3 grid(parts, a.H), block(Block<LPR>::kThreads);
+  norm_bwd_kernel<IO, W, LPR, NV, A, kPlain><<<grid, block, lds, s>>>(a, part, share);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !sums) return e;
   norm_sum_kernel<<<dim3((a.d + 31) / 32, a.H, 3), dim3(1024), 0, s>>>(a, part, parts);
@@ -570,7 +577,9 @@ hipError_t bwd_io(const NormArgs& a, void* ws, hipStream_t s) {
 
 template <typename IO>
 hipError_t fwd_io(const NormArgs& a, hipStream_t s) {
-  return choose<IO, false>(a, [&](auto w, auto lpr, auto nv, auto al) { return run_fwd<IO, w.value, lpr.value, nv.value, al.value>(a, s); });
+  return choose<IO, false>(a, [&](auto w, auto lpr, auto nv, auto al) {
+    return run_fwd<IO, w.value, lpr.value, nv.value, al.value>(a, s);
+  });
 }
 
 }  // namespace
