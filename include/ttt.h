@@ -359,23 +359,23 @@ int ttt_mlp_nc_bwd(const void* q, const void* k, const void* v,
  * attention) with a decay per token and head; with a constant decay the retention recurrence
  * S_t = alpha S_{t-1} + k_t v_t^T (same page), without a gate the dot-product loss at chunk 1.
  *   log_gate   float32 [B][H][T] or NULL (no decay).  Usually <= 0; -inf (or any value whose
- *              exponential is 0 in float32) makes the token start anew: what the state held
- *              before, finite or not, is dropped.  So packed sequences are separated by a
- *              gate of -inf at each one's first token.
+ *              exponential is below float32's smallest normal number, 2^-126) makes the
+ *              token start anew: what the state held before, finite or not, is dropped.  So
+ *              packed sequences are separated by a gate of -inf at each one's first token.
  *   lengths    int32 [B] device pointer or NULL: batch row b has min(max(lengths[b], 0), T)
  *              tokens.  Tokens past them are not read; their outputs and gradients are 0.
  *   q, k, v, dz of tokens within the lengths are finite; a token that is not may make any output
  *   of its sequence non-finite (forward up to a gate of -inf in a later block of 64 tokens).
- * d in {16, 32, 64}, both dtypes, 0 <= T <= 2^30 (T = 0: w_out receives the initial state), B*H*d
- * < 2^29, B*H*(T/64 + 1) < 2^31 (more is TTT_E_UNSUPPORTED).  Token
- * tensors, states, their gradients and the workspace are 16-byte aligned, w0_batch_stride is
- * a multiple of 4 (TTT_E_INVALID otherwise); eta_tok, log_gate and lengths 4-byte aligned.
+ * d in {16, 32, 64}, both dtypes, 0 <= T <= 2^30 (T = 0: w_out receives the initial state),
+ * B*H*d < 2^29, B*H*(T/64 + 1) < 2^31 (more is TTT_E_UNSUPPORTED).  Token tensors, states, their
+ * gradients and the workspace are 16-byte aligned, w0_batch_stride is a multiple of 4
+ * (TTT_E_INVALID otherwise); eta_tok, log_gate and lengths 4-byte aligned.
  * The states and every sum are float32; bf16 inputs are multiplied exactly.
  *
  * gated_linear_bwd is the backward pass for the upstream gradients dz of z and dw_out of the
  * final state (float32 [B][H][d][d] or NULL, zero): dq, dk, dv [B][H][T][d] io_dtype,
  *   dw0       float32 [B][H][d][d], per sequence (sum over b for a state shared over the batch)
- *   dlog_gate float32 [B][H][T] or NULL (needs log_gate); 0 where the decay is 0
+ *   dlog_gate float32 [B][H][T] or NULL (needs log_gate); 0 where the token starts anew
  *   deta_tok  float32 [B][H][T] or NULL (needs eta_tok).
  * It needs no output of the forward pass.
  *

@@ -25,10 +25,11 @@ struct GlDecays {
   float whole[4];                    // exp(b_C) (first entry)
 };
 
-// Base-2 logarithms below kGlNever count as kGlNever: 2^-4096 is 0 in float32 as the decay
-// itself is, and sums over a chunk stay below 2^18, so that two floats hold them to 2^-29 and
-// tokens after a forgotten one (g = -inf, or the type's lowest value) keep exact differences.
-constexpr double kGlNever = -4096.0;
+// Base-2 logarithms below kGlLeast, whose decays float32 flushes to 0, count as kGlNever: whatever
+// growth (g > 0) follows in the chunk does not bring back what they drop, and sums over a
+// chunk stay below 2^18, so that two floats hold them to 2^-29 and tokens after a forgotten one (g =
+// -inf, or the type's lowest value) keep exact differences.
+constexpr double kGlLeast = -126.0, kGlNever = -4096.0;
 
 // two floats rounded to bf16 in one word, and the floats that a word holds
 __device__ __forceinline__ uint32_t gl_pack(float lo, float hi) {
@@ -66,7 +67,7 @@ __device__ __forceinline__ double gl_prefix(double x) {
 // bits: b_u - b_s is a small difference of sums that may be large.
 __device__ __forceinline__ void gl_decays(float g, float e, bool live, GlDecays* d, int lane) {
   double x = static_cast<double>(g) * 1.4426950408889634;
-  if (x < kGlNever) x = kGlNever;  // a NaN stays one
+  if (x < kGlLeast) x = kGlNever;  // a NaN stays one
   x = gl_prefix(x);
   const double last = __shfl(x, kGlChunk - 1, 64);
   const float h = static_cast<float>(x), to = live ? __builtin_amdgcn_exp2f(static_cast<float>(last - x)) : 0.0f;

@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256) void gl_step_kernel(GatedArgs a, float* w) {
   float decay = 1.0f;
   if (a.gate) {
     double g = static_cast<double>(a.gate[chain]) * 1.4426950408889634;
-    if (g < kGlNever) g = kGlNever;
+    if (g < kGlLeast) g = kGlNever;
     decay = __builtin_amdgcn_exp2f(static_cast<float>(g));
   }
   const float e = a.eta_tok ? a.eta * a.eta_tok[chain] : a.eta;

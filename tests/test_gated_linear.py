@@ -233,6 +233,23 @@ def test_no_gradient_of_a_gate_whose_decay_is_zero(io, T):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_growth_does_not_bring_back_what_a_token_forgot(io):
+    x = gated_inputs(1, 2, 64, 32, io, "soft", seed=28)
+    x["v"][:] = 0
+    x["log_gate"][:] = 1.5
+    x["log_gate"][..., 10] = -90.0  # 2^-130; times exp(53 * 1.5) it would be large
+    g = _to_gpu(x)
+    z, w = _forward(g)
+    assert z[:, :, :10].any() and not z[:, :, 10:].any() and not w.any()
+    assert not _backward(g, with_dw_out=False)["dw0"][0, 0].isnan().any()
+    state = torch.ones((1, 2, 32, 32), device="cuda")
+    ttt.gated_linear_step(*(g[n][:, :, 10].contiguous() for n in "qkv"), state, g["eta"],
+                          g["log_gate"][:, :, 10].contiguous())
+    assert not state.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("T", [40, 700])
 def test_rates_without_a_gate(io, T):
     _check(gated_inputs(2, 2, T, 64, io, "none", rates=True, seed=23))
